@@ -14,6 +14,13 @@
  *   dflash_ctx_table,       the pages' context-gated pair scorer: its
  *   dflash_ctx_gate,        token tables, its gate, then its scores and a
  *   dflash_ctx_walk         walk
+ * and what a serving program needs around a cycle:
+ *   dflash_rmsnorm,         the norm in front of the LM head (bf16, or int8
+ *   dflash_rmsnorm_i8         with a scale per row)
+ *   dflash_quant_i8,        weights and activations in int8, and their
+ *   dflash_gemm_i8            product
+ *   dflash_token_logprobs,  log-probabilities of given tokens, or of the
+ *   dflash_emitted_logprobs   tokens a verification step emitted
  *
  * Sources: "DFlash 2: Keep Drafting Parallel" (the blog, read in its Chinese
  * translation) and "Inco AI's DFlash 2 lifts LLM decoding output 16-25%".
@@ -377,6 +384,118 @@ int dflash_ctx_walk(const float* topk_logp, const int32_t* topk_idx, const int32
  */
 int dflash_verify(const int32_t* draft, const int32_t* target, int B, int L, int32_t* accept_len,
                   int32_t* next_token, void* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition.
+ * The norm that makes the LM head's input H; the paper has no counterpart to
+ * this entry point (its drafter's layers are not published).  Per row m:
+ *   h = bf16(x + residual)   (fp32 sum, rounded to nearest even; h = x
+ *                             without a residual)
+ *   r = 1 / sqrt(mean_c h[c]^2 + eps)            (fp32)
+ *   y[c] = bf16(h[c] * gamma[c] * r)
+ * x, residual, h, y [M, d] bf16; gamma [d] bf16; residual NULL: none, and h
+ * must be NULL then; h NULL: the sum is not written.  h and y may each be the
+ * same array as x or as residual (not each other); any other overlap is not
+ * allowed.  A sum of squares beyond fp32's range is taken in fp64.
+ * Requires M >= 1, 8 <= d <= 32768, d % 8 == 0, eps finite and >= 1e-20,
+ * 16-byte aligned pointers.
+ */
+int dflash_rmsnorm(const dflash_bf16* x, const dflash_bf16* residual, const dflash_bf16* gamma, float eps, int M,
+                   int d, dflash_bf16* h, dflash_bf16* y, void* stream);
+
+/*
+ * The same norm with its output in int8 and one scale per row, as
+ * dflash_gemm_i8 takes it (no counterpart in the paper).  With
+ * a = max_c |h[c] * gamma[c]|:
+ *   scale = a * r / 127,  q[c] = rint(127 * h[c] * gamma[c] / a)
+ * (r cancels in q; halves round to even, decided exactly), so that
+ * q * scale is the normalised row to within half a step.  q is in
+ * [-127, 127].  A row with a < 2^-100 gives q = 0 and scale = 0; a row that
+ * holds a NaN or an infinity (after the product with gamma) gives q = 0 and
+ * scale = NaN, which a product taken from it carries on.
+ * q [M, d] int8 (8-byte aligned), scale [M] fp32; the rest as dflash_rmsnorm.
+ */
+int dflash_rmsnorm_i8(const dflash_bf16* x, const dflash_bf16* residual, const dflash_bf16* gamma, float eps, int M,
+                      int d, dflash_bf16* h, int8_t* q, float* scale, void* stream);
+
+/*
+ * Rows to int8 with one scale each: dflash_rmsnorm_i8 without the norm
+ * (h = x, gamma = 1, r = 1; no counterpart in the paper).  Lays a weight
+ * matrix out for dflash_gemm_i8 (a scale per output channel), or quantises
+ * activations that are normed already.  x [M, d] bf16, q [M, d] int8,
+ * scale [M] fp32; sizes and alignment as dflash_rmsnorm_i8.
+ */
+int dflash_quant_i8(const dflash_bf16* x, int M, int d, int8_t* q, float* scale, void* stream);
+
+/*
+ * Matrix product in 8-bit integers with a scale per token and per channel
+ * (the 8-bit counterpart of dflash_gemm_bf16; none in the paper):
+ *   C[m,n] = float(sum_k A[m,k] * B[n,k]) * sa[m] * sb[n]
+ * The sum is exact in int32 (K <= 131071 cannot overflow it); it is rounded
+ * once to fp32 and each product with a scale rounds once more, then once to
+ * the output type.  Scales are used as they are (a NaN scale makes its row or
+ * column NaN).
+ * A [M, K], B [N, K] int8 (K-major, 16-byte aligned), sa [M], sb [N] fp32
+ * (4-byte aligned), C [M, N] row-major: fp32 (c_bf16 == 0) or bf16
+ * (c_bf16 == 1), aligned to its element.  M, N >= 1, 16 <= K <= 131071,
+ * K % 16 == 0; C must not overlap an input.  Needs no workspace; results are
+ * the same bit for bit from run to run.
+ */
+int dflash_gemm_i8(const int8_t* A, const float* sa, const int8_t* B, const float* sb, void* C, int c_bf16, int M,
+                   int N, int K, int* dev_status, void* stream);
+
+/*
+ * Log-probabilities of given tokens, with entropy, rank and the top
+ * alternatives, from logits in memory (no counterpart in the paper; a
+ * serving program answers with them).  Row m, z = logits[m*ld .. m*ld + V):
+ *   lse      = log sum_v exp(z[v] / T)
+ *   logp     = z[t] / T - lse,  t = tokens[m]
+ *   rank     = 1 + number of v with z[v] > z[t]
+ *   entropy  = -sum_v p[v] log p[v],  p = exp(z / T - lse)   (nats)
+ *   top_idx  = the K largest z, value descending, ties to the lowest index;
+ *   top_logp = their log-probabilities
+ * With K = 16 top_logp and top_idx are the candidate lists
+ * dflash_path_select and the walks take.
+ *
+ * logits: fp32 (z_bf16 == 0) or bf16 (z_bf16 == 1) rows of V elements, ld
+ * elements apart (ld >= V), aligned to the element.  -inf masks a token
+ * (log-probability -inf, no entropy); in a row with nothing but -inf, lse and
+ * every log-probability are -inf, the entropy is 0.  A NaN or +inf in a row
+ * makes its lse, entropy and log-probabilities NaN; a NaN counts as the
+ * largest value in top_idx.
+ * tokens [M] int32: a negative one marks a row that is not asked for (padding
+ * of a batch): it is not read, and its outputs keep what they held.  A token
+ * >= V records DFLASH_ERR_BAD_INDEX; its row gets logp = NaN and rank = 0 and
+ * the rest as usual.  tokens NULL: no tokens (every row is asked for; logp
+ * and rank must be NULL).
+ * logp, entropy, lse [M] fp32, rank [M] int32, top_logp [M, K] fp32, top_idx
+ * [M, K] int32; every output is nullable (top_logp and top_idx: both or
+ * neither; neither when K == 0).  1 <= M, 1 <= V <= 16777216,
+ * 0 <= K <= min(32, V), T = temperature > 0 and finite.  Sums are fp32 within
+ * a thread (at most a few thousand terms) and fp64 across threads; results
+ * are the same bit for bit from run to run.
+ */
+int dflash_token_logprobs(const void* logits, int z_bf16, long long ld, int M, int V, const int32_t* tokens,
+                          float temperature, int K, float* logp, int32_t* rank, float* entropy, float* lse,
+                          float* top_logp, int32_t* top_idx, int* dev_status, void* stream);
+
+/*
+ * dflash_token_logprobs for the tokens a verification step emits: block b's
+ * rows b*(L+1) + i of target_logits (as dflash_verify_rejection takes them,
+ * or bf16, or ld elements apart) with
+ *   token = draft[b,i] for i < accept_len[b] - 1,
+ *   token = next_token[b] for i = accept_len[b] - 1;
+ * rows behind that are not read and their outputs keep what they held.
+ * draft [B, L], accept_len, next_token [B] int32 as dflash_verify and
+ * dflash_verify_rejection give them; an accept_len outside [1, L+1] records
+ * DFLASH_ERR_BAD_INDEX and is clamped; a token outside [0, V) records it too,
+ * its row as dflash_token_logprobs says.  Outputs [B, L+1] and [B, L+1, K].
+ * 1 <= B, 1 <= L <= 32.
+ */
+int dflash_emitted_logprobs(const void* target_logits, int z_bf16, long long ld, int B, int L, int V,
+                            const int32_t* draft, const int32_t* accept_len, const int32_t* next_token,
+                            float temperature, int K, float* logp, int32_t* rank, float* entropy, float* lse,
+                            float* top_logp, int32_t* top_idx, int* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

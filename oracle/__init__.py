@@ -41,6 +41,13 @@ Pins (``tests/test_oracle_*.py``, run with ``-m "not gpu"``):
                 hand cases, and the output-distribution theorem: the first
                 emitted token is distributed exactly as the target's p_0
                 (integrated over grids of both uniforms)
+  rmsnorm / rmsnorm_i8 / quant_i8
+                hand-worked rows, exact rational rounding of every quotient
+                (halves included), unit and sign rows
+  gemm_i8       exact integer sums by Python integers, the extreme values
+  token_logprobs / emitted_tokens
+                exact decimal log-probabilities, uniform and one-hot rows,
+                masks, ties, a planted shift by one position
 """
 from .conv import conv2tap, conv2tap_dynamic
 from .lmhead import logits, lmhead_topk, argmax_tokens, topk_margin_ok
@@ -48,8 +55,13 @@ from .selector import pair_scores, viterbi, viterbi_two_best, path_select
 from .verify import verify
 from .ctx_scorer import ctx_tables, ctx_select, maxsum_walk_tables
 from .walks import anchor_scores, greedy_walk, sample_walk, verify_rejection, inverse_cdf, target_probs
+from .norm import rmsnorm, rmsnorm_i8, quant_i8, residual_sum
+from .gemm_i8 import gemm_i8
+from .logprobs import token_logprobs, emitted_tokens, row_logprobs
 
 __all__ = ["conv2tap", "conv2tap_dynamic", "logits", "lmhead_topk", "argmax_tokens", "topk_margin_ok",
            "pair_scores", "viterbi", "viterbi_two_best", "path_select", "verify",
            "anchor_scores", "greedy_walk", "sample_walk", "verify_rejection", "inverse_cdf",
-           "target_probs", "ctx_tables", "ctx_select", "maxsum_walk_tables"]
+           "target_probs", "ctx_tables", "ctx_select", "maxsum_walk_tables",
+           "rmsnorm", "rmsnorm_i8", "quant_i8", "residual_sum", "gemm_i8", "token_logprobs", "emitted_tokens",
+           "row_logprobs"]
