@@ -39,6 +39,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "host_util.cuh"
 
 namespace dflash {
 namespace lm {
@@ -942,61 +943,6 @@ __global__ void __launch_bounds__(NT) merge_kernel_rank(const Partial* __restric
 
 // ------------------------------------------------------------ host side ----
 
-static int num_sms_current() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  return n;
-}
-
-// Budget of every mbarrier wait of one launch.  DFLASH_TIMEOUT_NS, read at
-// every call (a positive count of nanoseconds; a process may change it
-// between calls), takes precedence over DFLASH_TIMEOUT_MS, read once per
-// process; without either the budget is 2 s.
-static unsigned long long timeout_ns_from_env() {
-  if (const char* e = std::getenv("DFLASH_TIMEOUT_NS")) {
-    const long long ns = std::atoll(e);
-    if (ns > 0) return static_cast<unsigned long long>(ns);
-  }
-  static unsigned long long v = [] {
-    const char* e = std::getenv("DFLASH_TIMEOUT_MS");
-    long long ms = e ? std::atoll(e) : 2000;
-    if (ms <= 0) ms = 2000;
-    return static_cast<unsigned long long>(ms) * 1000000ull;
-  }();
-  return v;
-}
-
-// Tuning knobs, read at every call (unset: the defaults below).
-static int env_int(const char* name, int dflt, int lo, int hi) {
-  const char* e = std::getenv(name);
-  if (e == nullptr || e[0] == 0) return dflt;
-  int v = std::atoi(e);
-  return v < lo ? lo : (v > hi ? hi : v);
-}
-
-// Pairs (2-CTA MMA) are used unless DFLASH_PAIR=0 (read at every call).
-static bool pair_allowed() {
-  const char* e = std::getenv("DFLASH_PAIR");
-  return !(e != nullptr && e[0] == '0');
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return static_cast<EncodeTiledFn>(nullptr);
-    return reinterpret_cast<EncodeTiledFn>(ptr);
-  }();
-  return fn;
-}
-
 // 2-D bf16 tensor [rows, cols] row-major, box [box_rows, 64], 128-byte swizzle.
 static bool make_map(CUtensorMap* m, const void* base, int rows, int cols, int box_rows) {
   EncodeTiledFn fn = encode_fn();
@@ -1278,7 +1224,7 @@ static int launch(const dflash_bf16* H, const dflash_bf16* W, int M, int V, int 
 
 extern "C" size_t dflash_lmhead_topk_workspace(int M, int V, int d) {
   dflash::lm::Plan pl;
-  if (!dflash::lm::make_plan(M, V, d, dflash::lm::num_sms_current(), pl)) return 0;
+  if (!dflash::lm::make_plan(M, V, d, dflash::num_sms_current(), pl)) return 0;
   return dflash::lm::part_bytes(pl);
 }
 
@@ -1303,7 +1249,7 @@ extern "C" int dflash_gemm_bf16(const dflash_bf16* A, const dflash_bf16* B, floa
 
 extern "C" int dflash_lmhead_topk_records(int M, int V, int d) {
   dflash::lm::Plan pl;
-  if (!dflash::lm::make_plan(M, V, d, dflash::lm::num_sms_current(), pl)) return 0;
+  if (!dflash::lm::make_plan(M, V, d, dflash::num_sms_current(), pl)) return 0;
   return pl.p.P;
 }
 

@@ -51,6 +51,14 @@ def test_product(M, N, K):
     assert torch.equal(_run(A, sa, B, sb, torch.bfloat16).cpu(), want)
 
 
+@pytest.mark.parametrize("M,N,K", [(130, 300, 160), (256, 1000, 384), (300, 4099, 272), (1000, 777, 208)])
+def test_product_without_pairs(M, N, K, monkeypatch):
+    """DFLASH_PAIR=0 (read at every call): single CTAs on the tensor-bound path."""
+    monkeypatch.setenv("DFLASH_PAIR", "0")
+    A, sa, B, sb = _inputs(M, N, K, 5)
+    np.testing.assert_array_equal(_run(A, sa, B, sb).cpu().numpy(), oracle.gemm_i8(A, sa, B, sb))
+
+
 @pytest.mark.parametrize("M", [5, 200])
 def test_largest_sums(M):
     """Every product 128 * 128, K at its limit: the int32 sum reaches 2^31 - 2^18."""
