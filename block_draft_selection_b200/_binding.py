@@ -496,42 +496,42 @@ def dflash_lmhead_topk_merge(records, topk_logp=None, topk_idx=None, lse=None, s
 
 def _arg(t, name, dtype, shape, index):
     """The device pointer of a contiguous CUDA tensor of this type, shape and device."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
             and t.is_contiguous()):
-        _need(t, name, dtype, shape)
-        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
-    return t.data_ptr()
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
 
 
-class _Launch:
-    """Device and stream of one call: makes the tensors' device current for
-    its duration where it is not, and allocates on the launching stream."""
-    __slots__ = ("index", "stream", "ptr", "_guard")
+def _on(stream, index):
+    """The stream to launch on, as an integer."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device_index != index:
+        raise ValueError(f"stream must be on cuda:{index}, got cuda:{stream.device_index}")
+    return stream.cuda_stream
 
-    def __init__(self, index, stream):
-        self.index = index
-        if stream is not None and stream.device_index != index:
-            raise ValueError(f"stream must be on cuda:{index}, got cuda:{stream.device_index}")
-        self.stream = stream
-        self.ptr = (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream
-        self._guard = None
 
-    def new(self, dtype, shape, zero=False):
-        make = torch.zeros if zero else torch.empty
-        if self.stream is None:
-            return make(shape, dtype=dtype, device=f"cuda:{self.index}")
-        with torch.cuda.stream(self.stream):
-            return make(shape, dtype=dtype, device=f"cuda:{self.index}")
+def _new(dtype, shape, index, stream, make=torch.empty):
+    if stream is None:
+        return make(shape, dtype=dtype, device=index)
+    with torch.cuda.stream(stream):   # so that the allocator ties the memory to the stream that uses it
+        return make(shape, dtype=dtype, device=index)
 
-    def __enter__(self):
-        if torch.cuda.current_device() != self.index:
-            self._guard = torch.cuda.device(self.index)
-            self._guard.__enter__()
-        return self
 
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+def _call(name, index, *args):
+    """Call the entry point with the tensors' device current."""
+    if torch._C._cuda_getDevice() == index:
+        code = _FN[name](*args)
+    else:
+        with torch.cuda.device(index):
+            code = _FN[name](*args)
+    if code != DFLASH_OK:
+        raise DFlashError(name, code)
+
+
+_FN = {n: getattr(lib, n) for n in ("dflash_rmsnorm", "dflash_rmsnorm_i8", "dflash_quant_i8", "dflash_gemm_i8",
+                                    "dflash_token_logprobs", "dflash_emitted_logprobs")}
 
 
 def _matrix(t, name, dtype):
@@ -541,67 +541,58 @@ def _matrix(t, name, dtype):
     return t.shape
 
 
-def _norm(fn, x, gamma, residual, eps, h, stream, call):
-    M, d = _matrix(x, "x", torch.bfloat16)
+def _norm_inputs(x, gamma, residual, h, stream):
+    """(M, d, device index, pointers of x, residual, gamma and h, h)."""
+    M, d = shape = _matrix(x, "x", torch.bfloat16)
     index = x.get_device()
-    px = _arg(x, "x", torch.bfloat16, (M, d), index)
+    px = _arg(x, "x", torch.bfloat16, shape, index)
     pg = _arg(gamma, "gamma", torch.bfloat16, (d,), index)
-    run = _Launch(index, stream)
-    pr = ph = None
-    if residual is not None:
-        pr = _arg(residual, "residual", torch.bfloat16, (M, d), index)
-        if h is None:
-            h = run.new(torch.bfloat16, (M, d))
-        ph = _arg(h, "h", torch.bfloat16, (M, d), index)
-    elif h is not None:
-        raise ValueError("h is the sum with a residual: there is none")
-    with run:
-        _check(fn, call(run, px, pr, pg, float(eps), M, d, ph, run.ptr))
-    return h
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is the sum with a residual: there is none")
+        return M, d, index, px, None, pg, None, None
+    pr = _arg(residual, "residual", torch.bfloat16, shape, index)
+    if h is None:
+        h = _new(torch.bfloat16, shape, index, stream)
+    return M, d, index, px, pr, pg, _arg(h, "h", torch.bfloat16, shape, index), h
 
 
 def dflash_rmsnorm(x, gamma, residual=None, eps=1e-6, y=None, h=None, stream=None):
     """h = bf16(x + residual) (x without one), y = h * gamma / sqrt(mean h^2 + eps).
     x, residual [M,d], gamma [d] bf16 -> (y [M,d] bf16, h [M,d] bf16 or None without a residual).
     h and y may each be x or residual (an update in place), not each other."""
-    def call(run, px, pr, pg, eps, M, d, ph, st):
-        nonlocal y
-        if y is None:
-            y = run.new(torch.bfloat16, (M, d))
-        return lib.dflash_rmsnorm(px, pr, pg, eps, M, d, ph, _arg(y, "y", torch.bfloat16, (M, d), run.index), st)
-    h = _norm("dflash_rmsnorm", x, gamma, residual, eps, h, stream, call)
+    M, d, index, px, pr, pg, ph, h = _norm_inputs(x, gamma, residual, h, stream)
+    if y is None:
+        y = _new(torch.bfloat16, (M, d), index, stream)
+    _call("dflash_rmsnorm", index, px, pr, pg, eps, M, d, ph, _arg(y, "y", torch.bfloat16, (M, d), index),
+          _on(stream, index))
     return y, h
 
 
 def dflash_rmsnorm_i8(x, gamma, residual=None, eps=1e-6, q=None, scale=None, h=None, stream=None):
     """dflash_rmsnorm with its output in int8 and a scale per row (q * scale is the normalised row):
     (q [M,d] int8, scale [M] f32, h [M,d] bf16 or None without a residual)."""
-    def call(run, px, pr, pg, eps, M, d, ph, st):
-        nonlocal q, scale
-        if q is None:
-            q = run.new(torch.int8, (M, d))
-        if scale is None:
-            scale = run.new(torch.float32, (M,))
-        return lib.dflash_rmsnorm_i8(px, pr, pg, eps, M, d, ph, _arg(q, "q", torch.int8, (M, d), run.index),
-                                     _arg(scale, "scale", torch.float32, (M,), run.index), st)
-    h = _norm("dflash_rmsnorm_i8", x, gamma, residual, eps, h, stream, call)
+    M, d, index, px, pr, pg, ph, h = _norm_inputs(x, gamma, residual, h, stream)
+    if q is None:
+        q = _new(torch.int8, (M, d), index, stream)
+    if scale is None:
+        scale = _new(torch.float32, (M,), index, stream)
+    _call("dflash_rmsnorm_i8", index, px, pr, pg, eps, M, d, ph, _arg(q, "q", torch.int8, (M, d), index),
+          _arg(scale, "scale", torch.float32, (M,), index), _on(stream, index))
     return q, scale, h
 
 
 def dflash_quant_i8(x, q=None, scale=None, stream=None):
     """Rows x [M,d] bf16 -> (q [M,d] int8, scale [M] f32 = max|row| / 127)."""
-    M, d = _matrix(x, "x", torch.bfloat16)
+    M, d = shape = _matrix(x, "x", torch.bfloat16)
     index = x.get_device()
-    px = _arg(x, "x", torch.bfloat16, (M, d), index)
-    run = _Launch(index, stream)
+    px = _arg(x, "x", torch.bfloat16, shape, index)
     if q is None:
-        q = run.new(torch.int8, (M, d))
+        q = _new(torch.int8, shape, index, stream)
     if scale is None:
-        scale = run.new(torch.float32, (M,))
-    pq = _arg(q, "q", torch.int8, (M, d), index)
-    ps = _arg(scale, "scale", torch.float32, (M,), index)
-    with run:
-        _check("dflash_quant_i8", lib.dflash_quant_i8(px, M, d, pq, ps, run.ptr))
+        scale = _new(torch.float32, (M,), index, stream)
+    _call("dflash_quant_i8", index, px, M, d, _arg(q, "q", torch.int8, shape, index),
+          _arg(scale, "scale", torch.float32, (M,), index), _on(stream, index))
     return q, scale
 
 
@@ -613,23 +604,21 @@ def dflash_gemm_i8(A, sa, B, sb, C=None, dtype=torch.float32, dev_status=None, s
     if Kb != K:
         raise ValueError("A and B disagree on K")
     index = A.get_device()
-    pA = _arg(A, "A", torch.int8, (M, K), index)
-    pB = _arg(B, "B", torch.int8, (N, K), index)
-    psa = _arg(sa, "sa", torch.float32, (M,), index)
-    psb = _arg(sb, "sb", torch.float32, (N,), index)
-    run = _Launch(index, stream)
     if C is not None:
         dtype = C.dtype
     if dtype is not torch.float32 and dtype is not torch.bfloat16:
         raise TypeError(f"C must be {torch.float32} or {torch.bfloat16}, got {dtype}")
     if C is None:
-        C = run.new(dtype, (M, N))
-    pC = _arg(C, "C", dtype, (M, N), index)
-    pst = None if dev_status is None else _arg(dev_status, "dev_status", torch.int32, (1,), index)
-    with run:
-        _check("dflash_gemm_i8", lib.dflash_gemm_i8(pA, psa, pB, psb, pC, 1 if dtype is torch.bfloat16 else 0, M, N, K,
-                                                    pst, run.ptr))
+        C = _new(dtype, (M, N), index, stream)
+    _call("dflash_gemm_i8", index, _arg(A, "A", torch.int8, (M, K), index), _arg(sa, "sa", torch.float32, (M,), index),
+          _arg(B, "B", torch.int8, (N, K), index), _arg(sb, "sb", torch.float32, (N,), index),
+          _arg(C, "C", dtype, (M, N), index), 1 if dtype is torch.bfloat16 else 0, M, N, K,
+          _status(dev_status, index), _on(stream, index))
     return C
+
+
+def _status(dev_status, index):
+    return None if dev_status is None else _arg(dev_status, "dev_status", torch.int32, (1,), index)
 
 
 def _logits(z, name):
@@ -641,35 +630,41 @@ def _logits(z, name):
     if z.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got {z.dim()}")
     rows, V = z.shape
-    ld = z.stride(0) if rows > 1 else V
-    if (V > 1 and z.stride(1) != 1) or ld < V:
+    ld, step = z.stride()
+    if rows == 1:
+        ld = V
+    if (V > 1 and step != 1) or ld < V:
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
     return z.data_ptr(), 1 if z.dtype is torch.bfloat16 else 0, ld, rows, V, z.get_device()
 
 
-def _logprob_outs(run, shape, K, given, with_token):
-    """Outputs in the order logp, rank, entropy, lse, top_logp, top_idx and
-    their pointers.  What the call allocates is zeroed: rows that are not asked
-    for are not written."""
+def _logprob_out(t, name, dtype, shape, index, stream):
+    """An output and its pointer.  What the call allocates is zeroed: rows that are not asked for are not written."""
+    if t is None:
+        t = _new(dtype, shape, index, stream, torch.zeros)
+    return t, _arg(t, name, dtype, shape, index)
+
+
+def _logprob_outs(shape, K, index, stream, logp, rank, entropy, lse, top_logp, top_idx, with_token=True):
+    """Outputs in the order logp, rank, entropy, lse, top_logp, top_idx, and their pointers."""
     if not 0 <= K <= 32:
         raise ValueError(f"K must be in [0, 32], got {K}")
-    outs, ptrs = [], []
-    for name, t in given.items():
-        top = name.startswith("top_")
-        if not with_token and (name == "logp" or name == "rank"):
-            if t is not None:
-                raise ValueError(f"{name} needs tokens")
-            outs.append(None)
-            ptrs.append(None)
-            continue
-        dt = torch.int32 if name in ("rank", "top_idx") else torch.float32
-        sh = (*shape, K) if top else shape
-        if t is None:
-            t = run.new(dt, sh, zero=True)
-        ptr = _arg(t, name, dt, sh, run.index)
-        outs.append(t)
-        ptrs.append(None if top and K == 0 else ptr)
-    return tuple(outs), ptrs
+    f32, i32 = torch.float32, torch.int32
+    if with_token:
+        logp, p0 = _logprob_out(logp, "logp", f32, shape, index, stream)
+        rank, p1 = _logprob_out(rank, "rank", i32, shape, index, stream)
+    elif logp is not None or rank is not None:
+        raise ValueError("logp and rank need tokens")
+    else:
+        p0 = p1 = None
+    entropy, p2 = _logprob_out(entropy, "entropy", f32, shape, index, stream)
+    lse, p3 = _logprob_out(lse, "lse", f32, shape, index, stream)
+    top = (*shape, K)
+    top_logp, p4 = _logprob_out(top_logp, "top_logp", f32, top, index, stream)
+    top_idx, p5 = _logprob_out(top_idx, "top_idx", i32, top, index, stream)
+    if K == 0:
+        p4 = p5 = None
+    return (logp, rank, entropy, lse, top_logp, top_idx), (p0, p1, p2, p3, p4, p5)
 
 
 def dflash_token_logprobs(logits, tokens=None, K=K_TOP, temperature=1.0, logp=None, rank=None, entropy=None, lse=None,
@@ -680,13 +675,9 @@ def dflash_token_logprobs(logits, tokens=None, K=K_TOP, temperature=1.0, logp=No
     top_logp [M,K], top_idx [M,K] i32); logp and rank are None without tokens."""
     pz, z_bf16, ld, M, V, index = _logits(logits, "logits")
     pt = None if tokens is None else _arg(tokens, "tokens", torch.int32, (M,), index)
-    run = _Launch(index, stream)
-    outs, ptrs = _logprob_outs(run, (M,), K, {"logp": logp, "rank": rank, "entropy": entropy, "lse": lse,
-                                              "top_logp": top_logp, "top_idx": top_idx}, tokens is not None)
-    pst = None if dev_status is None else _arg(dev_status, "dev_status", torch.int32, (1,), index)
-    with run:
-        _check("dflash_token_logprobs", lib.dflash_token_logprobs(pz, z_bf16, ld, M, V, pt, float(temperature), K, *ptrs,
-                                                                  pst, run.ptr))
+    outs, ptrs = _logprob_outs((M,), K, index, stream, logp, rank, entropy, lse, top_logp, top_idx, tokens is not None)
+    _call("dflash_token_logprobs", index, pz, z_bf16, ld, M, V, pt, temperature, K, *ptrs,
+          _status(dev_status, index), _on(stream, index))
     return outs
 
 
@@ -697,20 +688,13 @@ def dflash_emitted_logprobs(target_logits, draft, accept_len, next_token, K=K_TO
     next_token [B] i32 and the target_logits [B*(L+1),V] they were verified against.  Outputs [B,L+1] (and
     [B,L+1,K]); positions at and past accept_len stay as they are (zero where the call allocates)."""
     pz, z_bf16, ld, rows, V, index = _logits(target_logits, "target_logits")
-    _need(draft, "draft", torch.int32)
-    if draft.dim() != 2:
-        raise ValueError(f"draft must have two dimensions, got {draft.dim()}")
-    B, L = draft.shape
+    B, L = _matrix(draft, "draft", torch.int32)
     if rows != B * (L + 1):
         raise ValueError(f"target_logits must have {B * (L + 1)} rows, got {rows}")
     pd = _arg(draft, "draft", torch.int32, (B, L), index)
     pa = _arg(accept_len, "accept_len", torch.int32, (B,), index)
     pn = _arg(next_token, "next_token", torch.int32, (B,), index)
-    run = _Launch(index, stream)
-    outs, ptrs = _logprob_outs(run, (B, L + 1), K, {"logp": logp, "rank": rank, "entropy": entropy, "lse": lse,
-                                                    "top_logp": top_logp, "top_idx": top_idx}, True)
-    pst = None if dev_status is None else _arg(dev_status, "dev_status", torch.int32, (1,), index)
-    with run:
-        _check("dflash_emitted_logprobs", lib.dflash_emitted_logprobs(
-            pz, z_bf16, ld, B, L, V, pd, pa, pn, float(temperature), K, *ptrs, pst, run.ptr))
+    outs, ptrs = _logprob_outs((B, L + 1), K, index, stream, logp, rank, entropy, lse, top_logp, top_idx)
+    _call("dflash_emitted_logprobs", index, pz, z_bf16, ld, B, L, V, pd, pa, pn, temperature, K, *ptrs,
+          _status(dev_status, index), _on(stream, index))
     return outs

@@ -4,42 +4,58 @@
 //   entropy = -sum p log p,  the K largest z (value desc, index asc)
 //
 // One pass over a row, which a cluster of Q CTAs shares (Q chosen so that few
-// rows still fill the GPU).  Each thread keeps a reference value `ref` (a
-// value near the largest it has seen), s = sum exp2(t) and w = sum t exp2(t)
-// with t = (z - ref) c, c = log2(e) / T, and the count of values above z_t.
-// The difference z - ref is taken first (exact near ref, where the terms that
-// matter are), so values as large as the type's range need no care, and equal
-// values give t = 0 exactly.  ref moves only when a value exceeds it by more
-// than LAG / c: terms up to 2^LAG cost no precision, and rescaling is rare.
+// rows still fill the GPU).  Each thread keeps a reference `base` (the largest
+// z c it has seen, or nearly), s = sum exp2(t) and w = sum t exp2(t) with
+// t = z c - base, c = log2(e) / T, one fused multiply-add, and the count of
+// values above z_t.  base is a value in fp32, not z c rounded: the results are
+// relative to it, so its rounding cancels.  It moves only when a value exceeds
+// it by more than LAG: terms up to 2^LAG cost no precision, and rescaling is
+// rare.  Where |base| would pass 1e29 (a row that holds nothing above a mask of
+// the type's lowest value, or an infinity) the row's sums are taken again from
+// differences z - max; values below -1e30 / c count as that value.
 //
 // c is rounded to fp32, i.e. the sums are those of a temperature off by a
 // relative 2^-24; the log of the sum is corrected for that to first order with
 // the mean of t, which the entropy needs anyway.
 //
+// The row streams through shared memory: each thread copies its own 16-byte
+// vectors (cp.async) S - 1 rounds ahead and reads them back itself, so the
+// loop has no barrier for its data, and the bytes in flight do not cost
+// registers.  (Bulk copies of a warp's whole chunk were measured instead: the
+// longer way through the copy engine costs more than the load instructions
+// saved, 31 against 19 us for 8 rows of 151936 on one CTA each.)
+//
 // Alternatives: K threads whose maxima are at least tau prove that the K-th
-// largest value is at least tau.  Each warp's ceil(K / 16)-th largest thread
-// maximum, and of those the least, is such a tau; it is found after rounds 1,
-// 2, 4, 8, ... of the loop from the running maxima, and a value below it costs
-// no more than the comparison of its round's maximum.  The few others (about
-// 70 a doubling on unsorted rows) go into their warp's list, sorted over the
-// lanes.  At the end the lists' entries above the last tau are ranked by
-// counting, first in each CTA, then in the cluster's first CTA, to which the
-// others write theirs through distributed shared memory.
+// largest value is at least tau.  The K-th largest of the warps' best thread
+// maxima (32 of them) is such a tau; it is found after rounds 1, 4, 16, ... of
+// the loop from the running maxima.  A thread whose round holds nothing of at
+// least tau is done with one comparison; the others (20 to 60 of them between
+// two bounds on unsorted rows for K = 16) note the round's maximum and its
+// number.  At the end the rounds with a maximum above the last tau are read
+// again and their values above it ranked by counting, first in each CTA, then
+// in the cluster's first CTA, to which the others write theirs through
+// distributed shared memory.  Rows that overflow these buffers (rising ones,
+// or with many values equal to the K-th) are read once more against the last
+// tau, into a list per warp that is sorted over its lanes.  Values of -inf are
+// never listed; where fewer than K others exist, the first -inf fill up.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "host_util.cuh"
 
 namespace dflash {
 namespace lp {
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int NT = 512;
-constexpr int NW = NT / 32;
 constexpr int MAX_K = 32;
 constexpr int MAX_V = 1 << 24;
-constexpr int MAX_Q = 16;           // CTAs that share a row: a cluster
-constexpr int ELEMS = 16;           // logits per thread and round
+constexpr int MAX_Q = 8;            // CTAs that share a row: a cluster
+constexpr int NOTES = 1024;         // rounds a CTA can note
+constexpr int LIST = 512;           // entries ranked at the end: as many as the warps' lists hold
 constexpr float LAG = 64.f;
+constexpr float FAR = 1e29f;        // |base| stops here: the row is far
+constexpr float LOW = -1e30f;       // terms below this z c are none
+constexpr uint32_t LOWEST_KEY = 0x00800000u;   // of the lowest finite value
 constexpr double LN2 = 0.69314718055994530942;
 
 struct Args {
@@ -48,13 +64,16 @@ struct Args {
   int V;
   int K;
   float c;           // log2(e) / T in fp32
+  float lo;          // LOW / c
   double inv_t;      // 1 / T
+  double per_t;      // 1 / (T c): nats per unit of t, ln 2 but for c's rounding
   const int32_t* tokens;      // given tokens (or NULL)
   const int32_t* draft;       // emitted tokens: draft [B, L], accept_len, next_token [B]
   const int32_t* accept_len;
   const int32_t* next_token;
   int L;
   int Q;
+  int eager;
   float* logp;
   int32_t* rank;
   float* entropy;
@@ -113,6 +132,7 @@ struct Vec<float> {
     x[2] = __uint_as_float(u.z);
     x[3] = __uint_as_float(u.w);
   }
+  static __device__ __forceinline__ float value(float v) { return v; }
   static __device__ __forceinline__ float load(const float* p) { return __ldg(p); }
   static __device__ __forceinline__ uint32_t bits(const float* p) { return __float_as_uint(__ldg(p)); }
 };
@@ -128,6 +148,7 @@ struct Vec<__nv_bfloat16> {
       x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
     }
   }
+  static __device__ __forceinline__ float value(__nv_bfloat16 v) { return __bfloat162float(v); }
   static __device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
 };
 
@@ -175,26 +196,125 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-// Sums relative to a reference: s = sum 2^t, w = sum t 2^t, t = (z - m) c.
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Two fp32 operations in one instruction.
+struct F2 {
+  uint64_t v;
+  F2() = default;
+  __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+// What a thread does with its N words of a round (fp32: one logit each; bf16:
+// two, for which maximum, minimum and count run packed).
+template <typename Z, int N>
+struct Round;
+
+template <int N>
+struct Round<float, N> {
+  static constexpr int PAIRS = N / 2;
+  float x[N];
+  __device__ __forceinline__ void set(int i, uint32_t w) { x[i] = __uint_as_float(w); }
+  __device__ __forceinline__ F2 pair(int i) const { return F2(x[2 * i], x[2 * i + 1]); }
+  __device__ __forceinline__ float largest() const {   // NaN if there is one
+    float m = x[0];
+#pragma unroll
+    for (int i = 1; i + 1 < N; i += 2) m = max_nan(m, max_nan(x[i], x[i + 1]));
+    return max_nan(m, x[N - 1]);
+  }
+  __device__ __forceinline__ void raise(float lo) {   // NaN stays
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = max_nan(x[i], lo);
+  }
+  __device__ __forceinline__ int above(float zt) const {
+    F2 n(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) n = add2(n, F2(one_if_above(x[i], zt), one_if_above(x[i + 1], zt)));
+    float a, b;
+    n.get(a, b);
+    return static_cast<int>(a + b);
+  }
+  static __device__ __forceinline__ float one_if_above(float a, float b) {
+    float r;
+    asm("set.gt.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+  }
+};
+
+template <int N>
+struct Round<__nv_bfloat16, N> {
+  static constexpr int PAIRS = N;
+  __nv_bfloat162 x[N];
+  __device__ __forceinline__ void set(int i, uint32_t w) { x[i] = *reinterpret_cast<const __nv_bfloat162*>(&w); }
+  __device__ __forceinline__ F2 pair(int i) const {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&x[i]);
+    return F2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+  __device__ __forceinline__ float largest() const {
+    __nv_bfloat162 m = x[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) m = __hmax2_nan(m, x[i]);
+    return max_nan(__low2float(m), __high2float(m));
+  }
+  __device__ __forceinline__ void raise(float lo) {
+    const __nv_bfloat162 l = __float2bfloat162_rn(lo);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __hmax2_nan(x[i], l);
+  }
+  __device__ __forceinline__ int above(float zt) const {   // counts up to N <= 256 are exact
+    const __nv_bfloat162 t = __float2bfloat162_rn(zt);
+    __nv_bfloat162 n = __hgt2(x[0], t);
+#pragma unroll
+    for (int i = 1; i < N; ++i) n = __hadd2(n, __hgt2(x[i], t));
+    return static_cast<int>(__low2float(n) + __high2float(n));
+  }
+};
+
+// Sums relative to a base (-inf: no values): s = sum 2^t, w = sum t 2^t,
+// t = z c - base.
 struct Sums {
-  float m;
+  float base;
   int cnt;
   double s, w;
 
-  // Over the warp: relative to the largest reference, then added in fp64.
-  __device__ __forceinline__ void reduce(float c) {
-    float big = m;
+  // Over groups of G lanes, relative to their largest base.
+  template <int G>
+  __device__ __forceinline__ void reduce() {
+    float big = base;
 #pragma unroll
-    for (int off = 16; off; off >>= 1) big = fmaxf(big, __shfl_xor_sync(FULL, big, off));
-    if (m != -INFINITY && m != big) {   // with m = -inf the sums are 0 (or NaN)
-      const float d = (m - big) * c;
+    for (int off = G / 2; off; off >>= 1) big = fmaxf(big, __shfl_xor_sync(FULL, big, off));
+    if (base != -INFINITY && base != big) {
+      const float d = base - big;
       const double f = ex2(d);
       w = f > 0.0 ? f * (w + d * s) : s * 0.0;
       s *= f;
     }
-    m = big;
+    base = big;
 #pragma unroll
-    for (int off = 16; off; off >>= 1) {
+    for (int off = G / 2; off; off >>= 1) {
       s += __shfl_xor_sync(FULL, s, off);
       w += __shfl_xor_sync(FULL, w, off);
       cnt += __shfl_xor_sync(FULL, cnt, off);
@@ -202,295 +322,508 @@ struct Sums {
   }
 };
 
-// The token asked for in a row, and whether the row is asked for at all.
-__device__ __forceinline__ bool row_token(const Args& p, int row, int& token) {
-  token = -1;
-  if (p.accept_len != nullptr) {
-    const int b = row / (p.L + 1), i = row - b * (p.L + 1);
-    int n = p.accept_len[b];
-    if (n < 1 || n > p.L + 1) {
-      if (threadIdx.x == 0) set_status(p.status, DFLASH_ERR_BAD_INDEX);
-      n = n < 1 ? 1 : p.L + 1;
-    }
-    if (i >= n) return false;
-    token = i == n - 1 ? p.next_token[b] : p.draft[static_cast<size_t>(b) * p.L + i];
-    if (token < 0) token = 0x7fffffff;   // out of range, not padding
-    return true;
-  }
-  if (p.tokens != nullptr) {
-    token = p.tokens[row];
-    return token >= 0;
-  }
-  return true;
+// 1 / x and log x of a positive finite fp64 sum, to about 1e-12 and 1e-7 of
+// log x's mantissa part: fp32 functions (log1p of mantissa - 1 keeps the
+// relative precision of sums just above 1), one Newton step for 1 / x.  A few
+// fp64 operations instead of the library's hundreds on a row's critical path.
+__device__ __forceinline__ double recip(double x) {
+  const double r = 1.f / static_cast<float>(x);
+  return r * (2.0 - x * r);
 }
 
-// Shared memory of a CTA; `all` and `sums` of the cluster's first CTA take
-// every CTA's list and sums.
+__device__ __forceinline__ double log_sum(double x) {
+  const int hi = __double2hiint(x);
+  int e = (hi >> 20) - 1023;
+  double mant = __hiloint2double((hi & 0x000fffff) | 0x3ff00000, __double2loint(x));   // [1, 2)
+  if (mant > 1.4142135) {
+    mant *= 0.5;
+    ++e;
+  }
+  return e * LN2 + static_cast<double>(log1pf(static_cast<float>(mant - 1.0)));
+}
+
+// The token asked for in a row: what it is read from, then what it is and
+// whether the row is asked for at all.
+struct RowToken {
+  int n = 0, next = -1, token = -1;
+
+  __device__ __forceinline__ void load(const Args& p, int row) {
+    if (p.accept_len != nullptr) {
+      const int b = row / (p.L + 1), i = row - b * (p.L + 1);
+      n = p.accept_len[b];
+      next = p.next_token[b];
+      if (i < p.L) token = p.draft[static_cast<size_t>(b) * p.L + i];
+    } else if (p.tokens != nullptr) {
+      token = p.tokens[row];
+    }
+  }
+  __device__ __forceinline__ bool asked(const Args& p, int row) {
+    if (p.accept_len != nullptr) {
+      const int i = row % (p.L + 1);
+      if (n < 1 || n > p.L + 1) {
+        if (threadIdx.x == 0) set_status(p.status, DFLASH_ERR_BAD_INDEX);
+        n = n < 1 ? 1 : p.L + 1;
+      }
+      if (i >= n) return false;
+      if (i == n - 1) token = next;
+      if (token < 0) token = 0x7fffffff;   // out of range, not padding
+      return true;
+    }
+    return p.tokens == nullptr || token >= 0;
+  }
+};
+
+// Shared memory of a CTA beside its ring; `all` and `sums` of the cluster's
+// first CTA take every CTA's list and sums.
 struct Shared {
-  uint64_t list[NW * 32];           // entries to be ranked
+  uint64_t note[NOTES];             // (key of the round's maximum, round * 32 + lane), per warp
+  uint64_t list[LIST];              // entries to be ranked
   uint64_t all[MAX_Q * MAX_K];      // [CTA][K], sorted downwards, 0 past the end
   Sums sums[MAX_Q];
-  Sums part[NW];
-  uint32_t tau[2][NW];
-  int n;
-  int n_all;
-  double log_s;
+  Sums part[16];
+  alignas(16) uint32_t best[2][32]; // keys of thread maxima, 32 / warps of each warp
+  int n_list, n_all;
+  double origin, base, log_s;       // z's log-probability: ((z - origin) c - base) per_t - log_s
 };
 
 // Rank the n entries of `list` by counting and hand each with its rank to put.
-template <typename F>
+template <int NW, typename F>
 __device__ __forceinline__ void rank_entries(const uint64_t* list, int n, int K, F put) {
-  for (int i = threadIdx.x; i < n; i += NT) {
+  for (int i = threadIdx.x; i < n; i += NW * 32) {
     const uint64_t mine = list[i];
     int rank = 0;
+#pragma unroll 8
     for (int k = 0; k < n; ++k) rank += list[k] > mine ? 1 : 0;
     if (rank < K) put(rank, mine);
   }
 }
 
-template <typename Z>
-__global__ void __launch_bounds__(NT, 2) logprobs_kernel(const Args p) {
+// The sums of a row from differences to its maximum, by one CTA: for rows
+// whose values times c leave fp32.  Returns the maximum; s and w in every
+// thread.
+template <typename Z, int NT>
+__device__ __noinline__ float far_sums(const Z* z, int V, float c, Shared& sh, double& s, double& w) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float m = -INFINITY;
+  for (int v = threadIdx.x; v < V; v += NT) m = fmaxf(m, Vec<Z>::load(z + v));
+  m = warp_max(m);
+  __syncthreads();
+  if (lane == 0) sh.part[warp].base = m;
+  __syncthreads();
+  for (int k = 0; k < NT / 32; ++k) m = fmaxf(m, sh.part[k].base);
+  s = w = 0.0;
+  for (int v = threadIdx.x; v < V; v += NT) {
+    const float t = max_nan((Vec<Z>::load(z + v) - m) * c, -200.f);
+    const float e = ex2(t);
+    s += e;
+    w += static_cast<double>(e) * t;
+  }
+  for (int off = 16; off; off >>= 1) {
+    s += __shfl_xor_sync(FULL, s, off);
+    w += __shfl_xor_sync(FULL, w, off);
+  }
+  if (lane == 0) {
+    sh.part[warp].s = s;
+    sh.part[warp].w = w;
+  }
+  __syncthreads();
+  s = w = 0.0;
+  for (int k = 0; k < NT / 32; ++k) {
+    s += sh.part[k].s;
+    w += sh.part[k].w;
+  }
+  return m;
+}
+
+// NT threads with U vectors each a round, S rounds in the ring.
+template <typename Z, int NT, int U, int S, int CTAS>
+__global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
   constexpr int E = Vec<Z>::E;
-  constexpr int U = ELEMS / E;      // vectors per thread and round
+  constexpr int NW = NT / 32;
+  constexpr int CAP = NOTES / NW;     // a warp's notes
+  constexpr int STAGE = U * NT;       // vectors per round
+  static_assert(NW * 32 <= LIST && NW <= 16 && MAX_Q * MAX_K <= LIST, "lists fit");
+  constexpr int CHUNK = U * 32;       // vectors per warp and round
+  extern __shared__ uint4 ring_all[];   // [NW][S][CHUNK]
   __shared__ Shared sh;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint4* ring = ring_all + warp * S * CHUNK;
+  const uint32_t ring_addr = smem_addr(ring + lane);
   const int Q = p.Q, row = blockIdx.x / Q, q = blockIdx.x - row * Q;
-  int token;
-  if (!row_token(p, row, token)) return;   // the same for every CTA of the cluster
-  // remote stores wait until every CTA of the cluster has started
-  if (Q > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  RowToken rt;
+  rt.load(p, row);
+  if (tid == 0) sh.n_list = sh.n_all = 0;
   const Z* z = static_cast<const Z*>(p.z) + static_cast<size_t>(row) * p.ld;
-  const bool bad_token = token >= p.V;
-  if (bad_token && tid == 0 && q == 0) set_status(p.status, DFLASH_ERR_BAD_INDEX);
 
   // the row as 16-byte vectors from the boundary at or before its start
   const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(Z));
   const int n_vec = (p.V + lead + E - 1) / E;
   const int v_begin = static_cast<int>(static_cast<long long>(q) * n_vec / Q);
   const int v_end = static_cast<int>(static_cast<long long>(q + 1) * n_vec / Q);
-  const int rounds = (v_end - v_begin + U * NT - 1) / (U * NT);
+  const int rounds = (v_end - v_begin + STAGE - 1) / STAGE;
   const uint32_t fill = E == 4 ? 0xff800000u : 0xff80ff80u;
-  uint4 nxt[U];
+  // vectors [in_begin, in_end) lie inside the row whole
+  const int in_begin = lead > 0 ? 1 : 0, in_end = min(v_end, (p.V + lead) / E);
+  const uint4* zv = reinterpret_cast<const uint4*>(z - lead);
+  const int w_begin = v_begin + warp * CHUNK;   // this warp's chunk of round 0
+  // This lane's copies of round r: its vectors that lie inside the row whole.
   auto fetch = [&](int r) {
+    const int v0 = w_begin + r * STAGE;
+    const uint32_t to = ring_addr + 16 * ((r % S) * CHUNK);
+    if (v0 >= in_begin && v0 + CHUNK <= in_end) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) copy16(to + 16 * u * 32, zv + v0 + u * 32 + lane);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int v = v0 + u * 32 + lane;
+        if (v >= in_begin && v < in_end) copy16(to + 16 * u * 32, zv + v);
+      }
+    }
+    copies_commit();
+  };
+  // this lane's vectors of round r
+  Round<Z, 4 * U> x;
+  auto take = [&](int r) {
+    const int v0 = w_begin + r * STAGE;
+    const uint4* at = ring + (r % S) * CHUNK + lane;
+    const bool whole = v0 >= in_begin && v0 + CHUNK <= in_end;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int v = v_begin + (r * U + u) * NT + tid;
-      nxt[u] = v < v_end ? load_vec(z, v * E - lead, p.V) : make_uint4(fill, fill, fill, fill);
+      const int v = v0 + u * 32 + lane;
+      uint4 vec;
+      if (whole || (v >= in_begin && v < in_end))
+        vec = at[u * 32];
+      else
+        vec = v < v_end ? load_vec(z, v * E - lead, p.V) : make_uint4(fill, fill, fill, fill);
+      x.set(4 * u, vec.x);
+      x.set(4 * u + 1, vec.y);
+      x.set(4 * u + 2, vec.z);
+      x.set(4 * u + 3, vec.w);
     }
   };
-  fetch(0);
-  const float zt = token >= 0 && !bad_token ? Vec<Z>::load(z + token) : 0.f;
-  if (tid == 0) sh.n = sh.n_all = 0;
+  // where every row's CTAs run at once, the first loads do not wait for the
+  // row's token (a row that is not asked for costs them in vain then)
+  if (p.eager) {
+#pragma unroll
+    for (int r = 0; r < S - 1; ++r) fetch(r);
+  }
+  if (!rt.asked(p, row)) {   // the same for every CTA of the cluster
+    copies_wait<0>();
+    return;
+  }
+  // remote stores wait until every CTA of the cluster has started
+  if (Q > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (!p.eager) {
+#pragma unroll
+    for (int r = 0; r < S - 1; ++r) fetch(r);
+  }
+  const bool bad_token = rt.token >= p.V;
+  if (bad_token && tid == 0 && q == 0) set_status(p.status, DFLASH_ERR_BAD_INDEX);
+  const float zt = rt.token >= 0 && !bad_token ? Vec<Z>::load(z + rt.token) : INFINITY;
 
-  float ref = -INFINITY, s = 0.f, w = 0.f, top_seen = -INFINITY, tau = -INFINITY;
-  int cnt = 0;
-  WarpTop top{0, 0};
-  int refreshed = 0;
-  auto refresh = [&]() {
-    const uint32_t key = key_of(top_seen);
-    uint32_t k = __reduce_max_sync(FULL, key);
-    if (p.K > NW) {   // the second largest
-      const bool first = lane == __ffs(__ballot_sync(FULL, key == k)) - 1;
-      k = __reduce_max_sync(FULL, first ? 0u : key);
+  const F2 c2(p.c, p.c);
+  F2 s2[2] = {F2(0.f, 0.f), F2(0.f, 0.f)}, w2[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
+  float base = 0.f, seen = -INFINITY, tau = -INFINITY;
+  uint32_t tau_key = 0;
+  int cnt = 0, bounds = 0, notes = 0, next_bound = 0;
+  // s and w relative to another base, d below
+  auto rescale = [](float d, float& s, float& w) {
+    const float f = ex2(d);
+    w = f > 0.f ? f * (w + d * s) : s * 0.f;
+    s *= f;
+  };
+  // Called by all threads: publish this warp's best maxima; after a barrier,
+  // the K-th largest of all.
+  auto publish = [&]() {
+    uint32_t left = key_of(seen);
+#pragma unroll
+    for (int i = 0; i < 32 / NW; ++i) {
+      const uint32_t k = __reduce_max_sync(FULL, left);
+      const int at = warp * (32 / NW) + i;
+      if (lane == 0) sh.best[bounds & 1][at] = (k & ~31u) | at;
+      if (lane == __ffs(__ballot_sync(FULL, left == k)) - 1) left = 0;
     }
-    uint32_t* t = sh.tau[refreshed++ & 1];
-    if (lane == 0) t[warp] = k;
-    __syncthreads();
-    k = __reduce_min_sync(FULL, t[lane & (NW - 1)]);
-    tau = value_of(static_cast<uint64_t>(k) << 32);
+  };
+  auto bound = [&]() {   // two buffers: a warp is at most one bound ahead of another
+    const uint4* best = reinterpret_cast<const uint4*>(sh.best[bounds & 1]);
+    const uint32_t mine = sh.best[bounds & 1][lane];
+    ++bounds;
+    int above = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint4 b = best[k];
+      above += (b.x > mine) + (b.y > mine) + (b.z > mine) + (b.w > mine);
+    }
+    // the low bits, which made the keys distinct, off: a little lower still bounds
+    tau_key = __shfl_sync(FULL, mine, __ffs(__ballot_sync(FULL, above == p.K - 1)) - 1) & ~31u;
+    tau = tau_key < LOWEST_KEY ? -INFINITY : value_of(static_cast<uint64_t>(tau_key) << 32);
   };
 
   for (int r = 0; r < rounds; ++r) {
-    float x[ELEMS];
+    copies_wait<S - 2>();
+    take(r);
+    fetch(r + S - 1);
+    const float m = x.largest();
+    if (m > seen) {
+      const float to = fminf(fmaxf(m * p.c, -FAR), FAR);
+      if (seen == -INFINITY) {
+        base = to;
+      } else if (to - base > LAG) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) Vec<Z>::unpack(nxt[u], x + u * E);
-    if (r + 1 < rounds) fetch(r + 1);
-    float gm[4];   // maxima of groups of four vectors' worth of a quarter of the round
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-      gm[g] = max_nan(max_nan(x[4 * g], x[4 * g + 1]), max_nan(x[4 * g + 2], x[4 * g + 3]));
-    const float m = max_nan(max_nan(gm[0], gm[1]), max_nan(gm[2], gm[3]));
-    top_seen = fmaxf(top_seen, m);
-    if (m > ref) {
-      if (ref == -INFINITY) {
-        ref = m;
-      } else if ((m - ref) * p.c > LAG) {
-        const float d = (ref - m) * p.c;
-        const float f = ex2(d);
-        w = f > 0.f ? f * (w + d * s) : s * 0.f;
-        s *= f;
-        ref = m;
+        for (int k = 0; k < 2; ++k) {
+          float s0, s1, w0, w1;
+          s2[k].get(s0, s1);
+          w2[k].get(w0, w1);
+          rescale(base - to, s0, w0);
+          rescale(base - to, s1, w1);
+          s2[k] = F2(s0, s1);
+          w2[k] = F2(w0, w1);
+        }
+        base = to;
       }
+      seen = m;
     }
-    const float base = ref == -INFINITY ? 0.f : ref;
-    float es[4], ws[4];
+    const bool bounding = p.K > 0 && r == next_bound;
+    if (bounding) publish();
+    if (m > zt || m != m) cnt += x.above(zt);
+    x.raise(p.lo);   // a masked value's t = -inf would make 0 * t a NaN
+    const F2 nb(-base, -base);
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      es[g] = ws[g] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // a masked value's t = -inf would make 0 * t a NaN; 2^-200 is 0
-        const float t = max_nan((x[4 * g + j] - base) * p.c, -200.f);
-        const float e = ex2(t);
-        es[g] += e;
-        ws[g] = fmaf(e, t, ws[g]);
-        cnt += x[4 * g + j] > zt ? 1 : 0;
-      }
+    for (int i = 0; i < x.PAIRS; ++i) {
+      const F2 t2 = fma2(x.pair(i), c2, nb);
+      float t0, t1;
+      t2.get(t0, t1);
+      const F2 e(ex2(t0), ex2(t1));
+      s2[i & 1] = add2(s2[i & 1], e);
+      w2[i & 1] = fma2(e, t2, w2[i & 1]);
     }
-    s += (es[0] + es[1]) + (es[2] + es[3]);
-    w += (ws[0] + ws[1]) + (ws[2] + ws[3]);
+    if (bounding) {
+      next_bound = 4 * r + 3;   // after 1, 4, 16, ... rounds
+      __syncthreads();
+      bound();
+    }
     if (p.K > 0) {
-      if ((r & (r + 1)) == 0) refresh();
-      if (__any_sync(FULL, !(m < tau))) {
+      const bool note = !(m < tau) && !(m == -INFINITY);
+      const unsigned who = __ballot_sync(FULL, note);
+      if (who) {
+        const int at = notes + __popc(who & ((1u << lane) - 1));
+        if (note && at < CAP)
+          sh.note[warp * CAP + at] = (static_cast<uint64_t>(key_of(m)) << 32) | static_cast<uint32_t>(r * 32 + lane);
+        notes += __popc(who);
+      }
+    }
+  }
+
+  // the warp's sums and the last bound
+  {
+    float s, w, s1, w1;
+    add2(s2[0], s2[1]).get(s, s1);
+    add2(w2[0], w2[1]).get(w, w1);
+    s += s1;
+    w += w1;
+    const float own = seen == -INFINITY ? -INFINITY : base;
+    const float big = warp_max(own);
+    if (own != -INFINITY && own != big) rescale(own - big, s, w);
+    // five levels in fp32, 2^-24 each; across warps and CTAs fp64
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          if (__any_sync(FULL, !(gm[g] < tau))) {
+    for (int off = 16; off; off >>= 1) {
+      s += __shfl_xor_sync(FULL, s, off);
+      w += __shfl_xor_sync(FULL, w, off);
+    }
+    cnt = __reduce_add_sync(FULL, cnt);
+    if (lane == 0) sh.part[warp] = Sums{big, cnt, s, w};
+  }
+  if (p.K > 0) publish();
+  __syncthreads();
+  Sums sum;
+  if (p.K > 0) {
+    bound();
+    // the noted rounds that still count, and their values: the round's vectors
+    // are read again (from the ring where the whole part is still in it)
+    for (int i = lane; i < min(notes, CAP); i += 32) {
+      const uint64_t e = sh.note[warp * CAP + i];
+      if (static_cast<uint32_t>(e >> 32) >= tau_key) {
+        const uint32_t id = static_cast<uint32_t>(e);
+        const int r = id / 32, ln = id % 32;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int el = 4 * g + j;
-              const int v = v_begin + (r * U + el / E) * NT + tid;
-              const int idx = v * E - lead + el % E;
-              const bool real = v < v_end && idx >= 0 && idx < p.V;
-              top.offer(real && !(x[el] < tau) ? entry_of(x[el], idx) : 0, p.K, lane);
+        for (int u = 0; u < U; ++u) {
+          const int at = u * 32 + ln, v = w_begin + r * STAGE + at;
+          uint4 vec = make_uint4(fill, fill, fill, fill);
+          if (rounds <= S && v >= in_begin && v < in_end)
+            vec = ring[r * CHUNK + at];
+          else if (v < v_end)
+            vec = load_vec(z, v * E - lead, p.V);
+          float x[E];
+          Vec<Z>::unpack(vec, x);
+#pragma unroll
+          for (int j = 0; j < E; ++j)
+            if (!(x[j] < tau) && !(x[j] == -INFINITY)) {
+              const int to = atomicAdd(&sh.n_list, 1);
+              if (to < LIST) sh.list[to] = entry_of(x[j], v * E - lead + j);
             }
-          }
         }
       }
     }
-  }
-
-  // sums of the warp, then of the CTA
-  Sums sum{ref, cnt, s, w};
-  sum.reduce(p.c);
-  if (lane == 0) sh.part[warp] = sum;
-  if (p.K > 0) {
-    refresh();
-    if (top.ent != 0 && static_cast<uint32_t>(top.ent >> 32) >= key_of(tau)) sh.list[atomicAdd(&sh.n, 1)] = top.ent;
-  }
-  __syncthreads();
-  if (Q > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  const uint32_t lead_all = Q > 1 ? mapa_shared(smem_addr(sh.all + q * MAX_K), 0) : smem_addr(sh.all);
-  if (warp == 0) {
-    sum = lane < NW ? sh.part[lane] : Sums{-INFINITY, 0, 0.0, 0.0};
-    sum.reduce(p.c);
-    if (lane == 0) {
-      if (Q > 1) {
-        const uint32_t to = mapa_shared(smem_addr(sh.sums + q), 0);
-        const uint64_t* from = reinterpret_cast<const uint64_t*>(&sum);
+    if (__syncthreads_or(notes > CAP) || sh.n_list > LIST) {   // the same for all threads
+      __syncthreads();
+      if (tid == 0) sh.n_list = 0;
+      WarpTop top{0, 0};
+      for (int v0 = w_begin; v0 < v_begin + rounds * STAGE; v0 += STAGE) {
+        for (int u = 0; u < U; ++u) {
+          const int v = v0 + u * 32 + lane;
+          float x[E];
+          Vec<Z>::unpack(v < v_end ? load_vec(z, v * E - lead, p.V) : make_uint4(fill, fill, fill, fill), x);
 #pragma unroll
-        for (int k = 0; k < static_cast<int>(sizeof(Sums) / 8); ++k) st_cluster_u64(to + 8 * k, from[k]);
-      } else {
-        sh.sums[0] = sum;
+          for (int j = 0; j < E; ++j)
+            top.offer(!(x[j] < tau) && !(x[j] == -INFINITY) ? entry_of(x[j], v * E - lead + j) : 0, p.K, lane);
+        }
       }
+      __syncthreads();
+      if (top.ent != 0) sh.list[atomicAdd(&sh.n_list, 1)] = top.ent;
+      __syncthreads();
     }
   }
-  if (p.K > 0) {
-    const int n = sh.n;
-    auto put = [&](int rank, uint64_t e) {
-      if (Q > 1)
-        st_cluster_u64(lead_all + 8 * rank, e);
-      else
-        sh.all[rank] = e;
-    };
-    rank_entries(sh.list, n, p.K, put);
-    if (tid >= n && tid < p.K) put(tid, 0);
+  // the CTA's sums by the first warp
+  if (warp == 0) {
+    sum = sh.part[lane & (NW - 1)];
+    sum.reduce<NW>();
   }
+  const int n_list = p.K > 0 ? sh.n_list : 0;
+
   if (Q > 1) {
+    // hand list and sums to the cluster's first CTA
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (tid == 0) {
+      const uint32_t to = mapa_shared(smem_addr(sh.sums + q), 0);
+      const uint64_t* from = reinterpret_cast<const uint64_t*>(&sum);
+#pragma unroll
+      for (int k = 0; k < static_cast<int>(sizeof(Sums) / 8); ++k) st_cluster_u64(to + 8 * k, from[k]);
+    }
+    if (p.K > 0) {
+      const uint32_t to = mapa_shared(smem_addr(sh.all + q * MAX_K), 0);
+      rank_entries<NW>(sh.list, n_list, p.K, [&](int rank, uint64_t e) { st_cluster_u64(to + 8 * rank, e); });
+      if (tid >= n_list && tid < p.K) st_cluster_u64(to + 8 * tid, 0);
+    }
     cluster_sync_all();
     if (q != 0) return;
-  } else {
-    __syncthreads();
+    if (warp == 0) {
+      const int i = lane & (MAX_Q - 1);
+      sum = i < Q ? sh.sums[i] : Sums{-INFINITY, 0, 0.0, 0.0};
+      sum.reduce<MAX_Q>();
+    }
+    if (p.K > 0) {
+      // the largest of the CTAs' K-th entries bounds the row's K-th from below
+      uint64_t least = lane < Q ? sh.all[lane * MAX_K + p.K - 1] : 0;
+#pragma unroll
+      for (int off = MAX_Q / 2; off; off >>= 1) {
+        const uint64_t o = __shfl_xor_sync(FULL, least, off);
+        least = o > least ? o : least;
+      }
+      least = __shfl_sync(FULL, least, 0);
+      for (int i = tid; i < Q * MAX_K; i += NT) {
+        const uint64_t e = (i & (MAX_K - 1)) < p.K ? sh.all[i] : 0;
+        if (e != 0 && e >= least) sh.list[atomicAdd(&sh.n_all, 1)] = e;
+      }
+    }
   }
 
-  // the row: sums of its CTAs by warp 0, alternatives by the others
-  if (warp == 0) {
-    sum = lane < Q ? sh.sums[lane] : Sums{-INFINITY, 0, 0.0, 0.0};
-    sum.reduce(p.c);
-    if (lane == 0) {
-      const double c = p.c;
-      const bool dead = sum.m == -INFINITY && sum.s == 0.0;
-      const double mean_t = sum.w / sum.s;
-      const double log_sum = log(sum.s);
-      // log of the sum relative to the maximum: every result is a difference
-      // to the reference plus this, which holds even where lse itself is near
-      // the type's lowest value
-      const double log_s = dead ? 0.0 : log_sum + (p.inv_t - c * LN2) * (mean_t / c);
-      sh.log_s = log_s;
-      sh.part[0].m = sum.m;
-      if (p.lse != nullptr) p.lse[row] = static_cast<float>(dead ? -INFINITY : sum.m * p.inv_t + log_s);
-      if (p.entropy != nullptr) p.entropy[row] = static_cast<float>(dead ? 0.0 : log_sum - mean_t * LN2);
-      if (p.logp != nullptr) {
-        const double v = dead ? -INFINITY : (static_cast<double>(zt) - sum.m) * p.inv_t - log_s;
-        p.logp[row] = bad_token ? __int_as_float(0x7fc00000) : static_cast<float>(v);
-      }
-      if (p.rank != nullptr) p.rank[row] = bad_token ? 0 : sum.cnt + 1;
+  // the row's results but for the alternatives, by one lane
+  double origin = 0.0;
+  if (__syncthreads_or(tid == 0 && !(fabsf(sum.base) < FAR) && sum.base != -INFINITY)) {
+    double s, w;
+    origin = far_sums<Z, NT>(z, p.V, p.c, sh, s, w);
+    sum.base = 0.f;
+    sum.s = s;
+    sum.w = w;
+  }
+  if (tid == 0) {
+    const bool dead = sum.base == -INFINITY && sum.s == 0.0;
+    const double from = dead ? 0.0 : sum.base;
+    const double mean_t = sum.w * recip(sum.s);
+    const double log_s0 = log_sum(sum.s);
+    const double log_s = dead ? 0.0 : log_s0 + (p.per_t - LN2) * mean_t;
+    sh.origin = origin;
+    sh.base = from;
+    sh.log_s = log_s;
+    if (p.lse != nullptr) p.lse[row] = static_cast<float>(dead ? -INFINITY : origin * p.inv_t + from * p.per_t + log_s);
+    if (p.entropy != nullptr) p.entropy[row] = static_cast<float>(dead ? 0.0 : log_s0 - mean_t * LN2);
+    if (p.logp != nullptr) {
+      const double v = ((zt - origin) * p.c - from) * p.per_t - log_s;
+      p.logp[row] = bad_token ? __int_as_float(0x7fc00000) : static_cast<float>(v);
     }
+    if (p.rank != nullptr) p.rank[row] = bad_token ? 0 : sum.cnt + 1;
   }
   if (p.K == 0) return;
-  if (Q > 1) {
-    // the largest of the CTAs' K-th entries bounds the row's from below
-    uint64_t bound = lane < Q ? sh.all[lane * MAX_K + p.K - 1] : 0;
-#pragma unroll
-    for (int off = 16; off; off >>= 1) {
-      const uint64_t o = __shfl_xor_sync(FULL, bound, off);
-      bound = o > bound ? o : bound;
-    }
-    if (tid < Q * MAX_K && (tid & (MAX_K - 1)) < p.K) {
-      const uint64_t e = sh.all[tid];
-      if (e != 0 && e >= bound) sh.list[atomicAdd(&sh.n_all, 1)] = e;
-    }
-  }
   __syncthreads();
-  const double log_s = sh.log_s;
-  const float m = sh.part[0].m;
+  const int n = Q > 1 ? sh.n_all : n_list;
   auto out = [&](int rank, uint64_t e) {
-    const float v = value_of(e);
     const size_t o = static_cast<size_t>(row) * p.K + rank;
-    p.top_logp[o] =
-        static_cast<float>(m == -INFINITY ? v + log_s : (static_cast<double>(v) - m) * p.inv_t - log_s);
+    p.top_logp[o] = static_cast<float>(((value_of(e) - sh.origin) * p.c - sh.base) * p.per_t - sh.log_s);
     p.top_idx[o] = index_of(e);
   };
-  if (Q > 1)
-    rank_entries(sh.list, sh.n_all, p.K, out);
-  else if (tid < p.K)
-    out(tid, sh.all[tid]);
-}
-
-// CTAs per row: enough to give every SM two, as long as each has a round.
-static int ctas_per_row(int rows, int V, int size) {
-  int q = 1;
-  while (q < MAX_Q && static_cast<long long>(rows) * q < 2 * 148 &&
-         static_cast<long long>(V) * size / (2 * q) >= NT * ELEMS * size / 2)
-    q *= 2;
-  return q;
-}
-
-static cudaError_t launch_rows(void (*kernel)(const Args), dim3 grid, dim3 block, const Args& a, cudaStream_t st) {
-  if (a.Q > 8) {   // beyond the portable cluster size
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
+  rank_entries<NW>(sh.list, n, p.K, out);
+  // fewer than K values that are not -inf: the first of -inf, by one warp
+  if (n < p.K && warp == NW - 1) {
+    int have = n;
+    for (int v0 = 0; have < p.K && v0 < p.V; v0 += 32) {
+      const int v = v0 + lane;
+      const bool none = v < p.V && Vec<Z>::load(z + v) == -INFINITY;
+      const unsigned which = __ballot_sync(FULL, none);
+      const int rank = have + __popc(which & ((1u << lane) - 1));
+      if (none && rank < p.K) out(rank, entry_of(-INFINITY, v));
+      have += __popc(which);
+    }
   }
-  return launch_kernel_cluster(kernel, grid, block, 0, st, a.Q, a);
+}
+
+template <typename Z, int NT, int U, int S, int CTAS>
+static cudaError_t launch_rows(int rows, const Args& a, cudaStream_t st) {
+  constexpr size_t bytes = sizeof(uint4) * S * U * NT;
+  auto* kernel = logprobs_kernel<Z, NT, U, S, CTAS>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e != cudaSuccess) return e;
+  return launch_kernel_cluster(kernel, dim3(static_cast<unsigned>(rows * a.Q)), dim3(NT), bytes, st, a.Q, a);
+}
+
+// Up to one row per SM: CTAs of 512 threads, one on an SM and all at once, with
+// as many of them to a row as fit (each with 4096 logits at least), and loads
+// that do not wait for the tokens.  More rows: three CTAs of 256 threads on an
+// SM, two to a row while all of them are resident together.  Rows of 151936
+// fp32, us, this rule's choice against the other form's best: 8 rows 9.9 / 11.1,
+// 32 rows 12.7 / 14.6, 64 rows 17.0 / 18.6, 148 rows 24.3 / 29.4; 200 rows 32.5
+// with two CTAs, 37.6 with one, 43.5 in the first form; 300 rows 47.8 with one,
+// 51.4 with two.  Clusters of 16 measured 16 us for 8 rows.
+template <typename Z>
+static cudaError_t launch_rows(int rows, Args& a, cudaStream_t st) {
+  const int sms = num_sms_current();
+  a.eager = rows <= sms;
+  a.Q = 1;
+  if (a.eager) {
+    while (a.Q < MAX_Q && 2 * a.Q * rows <= sms && a.V / (2 * a.Q) >= 4096) a.Q *= 2;
+    return launch_rows<Z, 512, 4, 3, 1>(rows, a, st);
+  }
+  if (2 * rows <= 3 * sms && a.V >= 2 * 4096) a.Q = 2;
+  return launch_rows<Z, 256, 4, 3, 3>(rows, a, st);
 }
 
 static int launch(Args& a, int z_bf16, int rows, float temperature, cudaStream_t st) {
   if (!a.z || (z_bf16 & ~1) || a.V < 1 || a.V > MAX_V || a.ld < a.V || a.K < 0 || a.K > MAX_K || a.K > a.V)
     return DFLASH_ERR_INVALID_ARG;
-  if (!(temperature > 0.f) || !(temperature < INFINITY)) return DFLASH_ERR_INVALID_ARG;
+  if (!(temperature >= 1e-6f) || !(temperature <= 1e6f)) return DFLASH_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(a.z) & (z_bf16 ? 1 : 3)) return DFLASH_ERR_INVALID_ARG;
   if ((a.top_logp == nullptr) != (a.top_idx == nullptr) || (a.top_logp != nullptr && a.K == 0))
     return DFLASH_ERR_INVALID_ARG;
   if (a.top_logp == nullptr) a.K = 0;
   a.inv_t = 1.0 / static_cast<double>(temperature);
   a.c = static_cast<float>(1.4426950408889634 / static_cast<double>(temperature));
-  if (!(a.c > 0.f) || !(a.c < INFINITY)) return DFLASH_ERR_INVALID_ARG;
-  a.Q = ctas_per_row(rows, a.V, z_bf16 ? 2 : 4);
-  if (rows > 0x7fffffff / a.Q) return DFLASH_ERR_INVALID_ARG;
-  const dim3 grid(static_cast<unsigned>(rows * a.Q)), block(NT);
-  const cudaError_t e = z_bf16 ? launch_rows(logprobs_kernel<__nv_bfloat16>, grid, block, a, st)
-                               : launch_rows(logprobs_kernel<float>, grid, block, a, st);
+  a.lo = LOW / a.c;
+  a.per_t = a.inv_t / a.c;
+  if (rows > 0x7fffffff / 2) return DFLASH_ERR_INVALID_ARG;
+  const cudaError_t e = z_bf16 ? launch_rows<__nv_bfloat16>(rows, a, st) : launch_rows<float>(rows, a, st);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 

@@ -54,7 +54,7 @@ def test_token_logprobs(lib):
     def call(z=OK, bf16=0, ld=100, M=4, V=100, tok=OK, T=1.0, K=16, logp=OK, rank=OK, ent=OK, lse=OK, tl=OK, ti=OK):
         return lib.dflash_token_logprobs(z, bf16, ld, M, V, tok, T, K, logp, rank, ent, lse, tl, ti, None, None)
     for bad in (dict(z=None), dict(bf16=2), dict(ld=99), dict(M=0), dict(V=0), dict(V=(1 << 24) + 1, ld=1 << 25),
-                dict(T=0.0), dict(T=-1.0), dict(T=float("inf")), dict(T=float("nan")), dict(K=-1), dict(K=33),
+                dict(T=0.0), dict(T=-1.0), dict(T=float("inf")), dict(T=float("nan")), dict(T=1e-7), dict(T=2e6), dict(K=-1), dict(K=33),
                 dict(K=16, V=10), dict(tok=None), dict(tok=None, logp=None), dict(tl=None), dict(ti=None), dict(K=0),
                 dict(z=OK + 2), dict(z=OK + 1, bf16=1)):
         assert call(**bad) == INVALID, bad
