@@ -42,6 +42,7 @@
 
 #include "common.cuh"
 #include "host_util.cuh"
+#include "pairs.cuh"
 
 namespace dflash {
 namespace lp {
@@ -177,13 +178,6 @@ __device__ __forceinline__ uint4 load_vec(const Z* z, int e0, int V) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The larger one; NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -211,23 +205,6 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Two fp32 operations in one instruction.
-struct F2 {
-  uint64_t v;
-  F2() = default;
-  __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-  __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-};
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
 // What a thread does with its N words of a round (fp32: one logit each; bf16:
 // two, for which maximum, minimum and count run packed).
 template <typename Z, int N>
@@ -271,7 +248,7 @@ struct Round<__nv_bfloat16, N> {
   __device__ __forceinline__ void set(int i, uint32_t w) { x[i] = *reinterpret_cast<const __nv_bfloat162*>(&w); }
   __device__ __forceinline__ F2 pair(int i) const {
     const uint32_t w = *reinterpret_cast<const uint32_t*>(&x[i]);
-    return F2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    return widen2(w);
   }
   __device__ __forceinline__ float largest() const {
     __nv_bfloat162 m = x[0];

@@ -6,55 +6,37 @@
 // One CTA per row; the row stays in registers (VPT vectors of 8 channels per
 // thread), so every input byte is read once.  r cancels in q, so the sum of
 // squares and the maximum come out of one block reduction and nothing waits
-// for r before the second pass over the registers.
+// for r before the second pass over the registers.  Memory bound: what counts
+// is bytes in flight.  Many rows take few threads with up to 8 vectors each,
+// all loaded before the first is used, and as many CTAs as fit on an SM; few
+// rows take one vector per thread, where the shortest chain counts.
 //
 // q is decided exactly.  h and gamma are bf16, so p = h * gamma has at most 16
-// significant bits and both p and 127 p are exact in fp32.  The quotient
-// 127 p / a differs from a halfway point k + 1/2, where it is not one, by a
-// relative 2^-15 / 254 or more (numerator and denominator are multiples of
-// 2^-15 of their leading bits), i.e. 1.2e-7, above the 2^-24 of a correctly
-// rounded division: rounding the IEEE quotient gives what rounding the real
-// one gives.  Without gamma (dflash_quant_i8) the operands have 8 bits and the
-// nearest miss is 2^-9 / 127 of q away, so a product with 127 / a decides as
-// exactly, provided that true halves stay halves or err upwards: those are
-// x = a/2 (q = 63.5, even neighbour 64) and, where a is 127 times a power of
-// two, exact products.  127 / a is therefore rounded up.
+// significant bits, and p, 127 p and q a (7 more bits) are exact in fp32; so
+// is their difference, which is below a.  q = rint(p (127 / a)), off by 2e-5
+// at most, is then the right one wherever |127 p - q a| < a / 2; elsewhere
+// (one value in 30000) the vector is divided out: 127 p / a differs from a
+// halfway point, where it is not one, by a relative 2^-16 / 254 = 6.01e-8 or
+// more (both sides are multiples of 2^-15 of their leading bits), above the
+// 2^-24 = 5.96e-8 of a correctly rounded division, so rounding the IEEE
+// quotient gives what rounding the real one gives.  Without gamma
+// (dflash_quant_i8) the operands have 8 bits and the nearest miss is 2^-9 / 127
+// of q away, so the product with 127 / a decides alone, provided that true
+// halves stay halves or err upwards: those are x = a/2 (q = 63.5, even
+// neighbour 64) and, where a is 127 times a power of two, exact products.
+// 127 / a is therefore rounded up.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "host_util.cuh"
+#include "pairs.cuh"
 
 namespace dflash {
 namespace norm {
 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int MAX_D = 32768;
-
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    f[2 * k] = __uint_as_float(w[k] << 16);
-    f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-  }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t lo = __bfloat16_as_ushort(__float2bfloat16_rn(f[2 * k]));
-    const uint32_t hi = __bfloat16_as_ushort(__float2bfloat16_rn(f[2 * k + 1]));
-    w[k] = lo | (hi << 16);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// The larger one; NaN if either is.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
+constexpr float MAGIC = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer, ties to even, in the low bits
 
 struct Args {
   const uint4* x;
@@ -68,64 +50,111 @@ struct Args {
   int d8;
 };
 
-template <int VPT, bool NORM, bool I8>
-__global__ void __launch_bounds__(1024) rmsnorm_kernel(const Args p) {
-  __shared__ float red_s[32], red_a[32];
-  __shared__ double red_d[32];
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+__device__ __forceinline__ uint32_t narrow2(F2 f) {
+  float a, b;
+  f.get(a, b);
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The low bytes of four words.
+__device__ __forceinline__ uint32_t bytes4(float a, float b, float c, float d) {
+  const uint32_t lo = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+
+// q of 8 values of p, the slow and exact way.
+__device__ __noinline__ uint2 divide8(uint4 h, uint4 g, float num, float den) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    mul2(widen2(word(h, i)), widen2(word(g, i))).get(a, b);
+    const uint32_t qa = __float2int_rn(__fdiv_rn(num * a, den)) & 0xff, qb = __float2int_rn(__fdiv_rn(num * b, den)) & 0xff;
+    w[i >> 1] |= (qa | (qb << 8)) << (16 * (i & 1));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// MINB: CTAs on an SM that the registers must allow.
+template <int VPT, int MAXT, int MINB, bool NORM, bool I8>
+__global__ void __launch_bounds__(MAXT, MINB) rmsnorm_kernel(const Args p) {
+  __shared__ float red_s[MAXT / 32], red_a[MAXT / 32];
+  __shared__ double red_d[MAXT / 32];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
   const size_t row = static_cast<size_t>(blockIdx.x) * p.d8;
   uint4 hv[VPT];
-  float ss = 0.f, a = 0.f;
+  {
+    uint4 rv[VPT];
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int c = tid + j * blockDim.x;
-    hv[j] = make_uint4(0, 0, 0, 0);
-    if (c < p.d8) {
-      hv[j] = p.x[row + c];
-      float f[8];
-      unpack8(hv[j], f);
-      if (NORM && p.res != nullptr) {
-        float g[8];
-        unpack8(p.res[row + c], g);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] += g[k];
-        hv[j] = pack8(f);
-        if (p.h != nullptr) p.h[row + c] = hv[j];
-        unpack8(hv[j], f);
+    for (int j = 0; j < VPT; ++j) {
+      const int c = tid + j * blockDim.x;
+      hv[j] = rv[j] = make_uint4(0, 0, 0, 0);
+      if (c < p.d8) {
+        hv[j] = p.x[row + c];
+        if (NORM && p.res != nullptr) rv[j] = p.res[row + c];
       }
-      if (NORM) {
+    }
+    if (NORM && p.res != nullptr) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) ss = fmaf(f[k], f[k], ss);
-      }
-      if (I8) {
-        if (NORM) {
-          float g[8];
-          unpack8(__ldg(p.gamma + c), g);
+      for (int j = 0; j < VPT; ++j) {
+        const int c = tid + j * blockDim.x;
+        uint32_t w[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] *= g[k];
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) a = max_nan(a, fabsf(f[k]));
+        for (int i = 0; i < 4; ++i) w[i] = narrow2(add2(widen2(word(hv[j], i)), widen2(word(rv[j], i))));
+        hv[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (p.h != nullptr && c < p.d8) p.h[row + c] = hv[j];
       }
     }
   }
+  F2 s2(0.f, 0.f);
+  float a = 0.f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = tid + j * blockDim.x;
+    uint4 g = make_uint4(0, 0, 0, 0);
+    if (NORM && I8 && c < p.d8) g = __ldg(p.gamma + c);
+    __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = word(hv[j], i);
+      const F2 f = widen2(w);
+      if (NORM) s2 = fma2(f, f, s2);
+      if (I8 && NORM) {
+        float u, v;
+        mul2(f, widen2(word(g, i))).get(u, v);
+        a = max_nan(a, fabsf(u));
+        a = max_nan(a, fabsf(v));
+      }
+      if (I8 && !NORM) m2 = __hmax2_nan(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+    }
+    if (I8 && !NORM) a = max_nan(a, max_nan(__low2float(m2), __high2float(m2)));
+  }
+  float ss, s1;
+  s2.get(ss, s1);
+  ss += s1;
 #pragma unroll
   for (int off = 16; off; off >>= 1) {
     if (NORM) ss += __shfl_xor_sync(FULL, ss, off);
     if (I8) a = max_nan(a, __shfl_xor_sync(FULL, a, off));
   }
-  if (lane == 0) {
-    red_s[warp] = ss;
-    red_a[warp] = a;
-  }
-  __syncthreads();
-  ss = 0.f;
-  a = 0.f;
-  for (int w = 0; w < nwarps; ++w) {
-    if (NORM) ss += red_s[w];
-    if (I8) a = max_nan(a, red_a[w]);
+  if (nwarps > 1) {
+    if (lane == 0) {
+      red_s[warp] = ss;
+      red_a[warp] = a;
+    }
+    __syncthreads();
+    ss = 0.f;
+    a = 0.f;
+    for (int w = 0; w < nwarps; ++w) {
+      if (NORM) ss += red_s[w];
+      if (I8) a = max_nan(a, red_a[w]);
+    }
   }
   const int d = p.d8 * 8;
   float r = 1.f;
@@ -137,10 +166,12 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const Args p) {
       double s = 0.0;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        float f[8];
-        unpack8(hv[j], f);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s = fma(static_cast<double>(f[k]), static_cast<double>(f[k]), s);
+        for (int i = 0; i < 4; ++i) {
+          float u, v;
+          widen2(word(hv[j], i)).get(u, v);
+          s = fma(static_cast<double>(u), static_cast<double>(u), fma(static_cast<double>(v), static_cast<double>(v), s));
+        }
       }
 #pragma unroll
       for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(FULL, s, off);
@@ -156,57 +187,77 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const Args p) {
     const bool zero = a < 7.8886091e-31f;   // 2^-100
     if (tid == 0) p.scale[blockIdx.x] = bad ? __int_as_float(0x7fc00000) : (zero ? 0.f : a * r / 127.f);
     const bool none = bad || zero;
-    const float inv = NORM || none ? 0.f : __fdiv_ru(127.f, a);
     // 127 p must stay in fp32's range: both sides of the quotient times a power of two
-    const float k = a > 1.2676506e30f ? 5.421010862e-20f : 1.f;   // 2^100, 2^-64
+    const float k = NORM && a > 1.2676506e30f ? 5.421010862e-20f : 1.f;   // 2^100, 2^-64
     const float num = 127.f * k, den = a * k;
+    const float inv = none ? 0.f : (NORM ? 127.f / a : __fdiv_ru(127.f, a));
+    const F2 inv2(inv, inv), num2(num, num), nden2(-den, -den), magic2(MAGIC, MAGIC), nmagic2(-MAGIC, -MAGIC);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int c = tid + j * blockDim.x;
-      if (c < p.d8) {
-        float f[8];
-        unpack8(hv[j], f);
-        uint32_t w[2] = {0, 0};
-        if (!none) {
-          float g[8];
-          if (NORM) unpack8(__ldg(p.gamma + c), g);
-#pragma unroll
-          for (int c8 = 0; c8 < 8; ++c8) {
-            const float t = NORM ? __fdiv_rn(num * (f[c8] * g[c8]), den) : f[c8] * inv;
-            w[c8 >> 2] |= (static_cast<uint32_t>(__float2int_rn(t)) & 0xffu) << (8 * (c8 & 3));
-          }
-        }
-        p.q[row + c] = make_uint2(w[0], w[1]);
+      if (c >= p.d8) continue;
+      if (none) {
+        p.q[row + c] = make_uint2(0, 0);
+        continue;
       }
+      uint4 g = make_uint4(0, 0, 0, 0);
+      if (NORM) g = __ldg(p.gamma + c);
+      float t[8], worst = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        F2 v = widen2(word(hv[j], i));
+        if (NORM) v = mul2(v, widen2(word(g, i)));
+        const F2 tm = fma2(v, inv2, magic2);
+        tm.get(t[2 * i], t[2 * i + 1]);
+        if (NORM) {
+          float e0, e1;
+          fma2(add2(tm, nmagic2), nden2, mul2(v, num2)).get(e0, e1);
+          worst = fmaxf(worst, fmaxf(fabsf(e0), fabsf(e1)));
+        }
+      }
+      uint2 q = make_uint2(bytes4(t[0], t[1], t[2], t[3]), bytes4(t[4], t[5], t[6], t[7]));
+      if (NORM && !(worst < 0.5f * den)) q = divide8(hv[j], g, num, den);
+      p.q[row + c] = q;
     }
   } else {
+    const F2 r2(r, r);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int c = tid + j * blockDim.x;
-      if (c < p.d8) {
-        float f[8], g[8];
-        unpack8(hv[j], f);
-        unpack8(__ldg(p.gamma + c), g);
+      if (c >= p.d8) continue;
+      const uint4 g = __ldg(p.gamma + c);
+      uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] = f[k] * g[k] * r;
-        p.y[row + c] = pack8(f);
-      }
+      for (int i = 0; i < 4; ++i) w[i] = narrow2(mul2(mul2(widen2(word(hv[j], i)), widen2(word(g, i))), r2));
+      p.y[row + c] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
 
+template <int VPT, int MAXT, int MINB, bool NORM, bool I8>
+static cudaError_t launch_as(const Args& a, int M, cudaStream_t st) {
+  const int threads = ((a.d8 + VPT - 1) / VPT + 31) & ~31;
+  return launch_kernel(rmsnorm_kernel<VPT, MAXT, MINB, NORM, I8>, dim3(static_cast<unsigned>(M)),
+                       dim3(static_cast<unsigned>(threads)), 0, st, a);
+}
+
+// At most one row per SM: one vector per thread ([8, 2560] int8 2.1 us, with two
+// vectors 2.3, with four 2.7; [64, 2560] 2.2, 2.4, 2.9).  More rows: two vectors
+// in the norm ([512, 2560] int8 3.2 us, with one 4.2, with four 4.5;
+// [4352, 4096] int8 23, 37, 30; bf16 23.6, 26.5, 24.0), four in the quantiser,
+// which holds no sum and no residual ([151936, 2560] 191 us, with one 316, with
+// two 207).
 template <bool NORM, bool I8>
 static int launch(const Args& a, int M, cudaStream_t st) {
-  const int vpt = a.d8 <= 512 ? 1 : (a.d8 <= 1024 ? 2 : 4);
-  const int threads = ((a.d8 + vpt - 1) / vpt + 31) & ~31;
-  const dim3 grid(static_cast<unsigned>(M)), block(static_cast<unsigned>(threads));
   cudaError_t e;
-  if (vpt == 1)
-    e = launch_kernel(rmsnorm_kernel<1, NORM, I8>, grid, block, 0, st, a);
-  else if (vpt == 2)
-    e = launch_kernel(rmsnorm_kernel<2, NORM, I8>, grid, block, 0, st, a);
+  if (a.d8 > 1024)
+    e = launch_as<4, 1024, 1, NORM, I8>(a, M, st);
+  else if (M <= num_sms_current())
+    e = launch_as<1, 1024, 1, NORM, I8>(a, M, st);
+  else if (NORM)
+    e = launch_as<2, 512, 3, NORM, I8>(a, M, st);
   else
-    e = launch_kernel(rmsnorm_kernel<4, NORM, I8>, grid, block, 0, st, a);
+    e = launch_as<4, 256, 5, NORM, I8>(a, M, st);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 
