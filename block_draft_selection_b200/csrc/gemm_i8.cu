@@ -8,28 +8,37 @@
 //   warp 1      MMA issuer into a double-buffered TMEM accumulator; owns the
 //               TMEM allocation
 //   warps 2..9  epilogue: TMEM -> registers -> C
-// The channels (rows of B) are on the MMA's M side and the tokens (rows of A)
-// on its N side.  A TMEM lane is then a channel and a register a token, so a
-// warp's store of one register is 32 consecutive elements of a row of C: full
-// 128-byte lines from any alignment of C, without a transpose.  And the tokens'
-// side has steps of 16 (32 in a pair) instead of 128: 448 tokens are two tiles
-// of 224.
-//   STREAM (M <= 128, bound by the bytes of B): one token tile of M rounded
-//          up to 16; each CTA owns one contiguous range of channels, balanced
-//          at 16 rows, cut into tiles of nearly equal height <= 128, so that
-//          no byte of B is read twice and all CTAs end together.
-//   LARGE  (M > 128): tiles of 256 channels x up to 256 tokens on a cluster
-//          of two CTAs that share one tcgen05.mma.cta_group::2 (each CTA
-//          stages half of either operand and receives its 128 channels), dealt
-//          out with the token tiles running fastest, so that the tiles in
-//          flight share few rows of B through L2.  DFLASH_PAIR=0: single CTAs
-//          with 128 channels.
+// A tcgen05.mma of M = 128 takes about 150 clocks whatever its N up to 128 or
+// so (measured: 600 a stage of four, on one accumulator or on four in turn), so
+// the operand whose bytes bound the call goes where an instruction takes more
+// of it, the N side:
+//   STREAM (M <= 128, bound by the bytes of B): channels (rows of B) on the N
+//          side, up to 256 a tile, the tokens (rows of A), rounded up to 16, on
+//          the M side.  (With the channels on the M side a stage of 16 KB took
+//          its 600 clocks, just the SM's share of the memory bandwidth.)  The
+//          tiles are dealt out as CTAs come to need them, since SMs do not get
+//          equal shares of the bandwidth: the grid has a CTA per tile, the
+//          first ones run, and each asks the hardware to cancel a CTA that has
+//          not started yet and takes its tile (cluster launch control).
+//          The accumulator's rows are tokens; the epilogue turns blocks of
+//          32 x 32 through shared memory and stores whole rows of them, from
+//          any alignment of C.
+//   LARGE  (M > 128): channels on the M side, tokens on the N side, in steps of
+//          32 instead of 128 (448 tokens are two tiles of 224).  Tiles of 256
+//          channels x up to 256 tokens on a cluster of two CTAs that share one
+//          tcgen05.mma.cta_group::2 (each CTA stages half of either operand and
+//          receives its 128 channels), dealt out with the token tiles running
+//          fastest, so that the tiles in flight share few rows of B through
+//          L2.  A TMEM lane is a channel and a register a token, so a warp's
+//          store of one register is 32 consecutive elements of a row of C
+//          without a transpose.  DFLASH_PAIR=0: single CTAs with 128 channels.
 // No load uses cluster multicast.  Every wait is bounded; a CTA that gives up
 // drains its copies as the LM-head kernel does (in a pair the leader, on whose
 // barriers both CTAs' copies complete, settles the stages that only one of
 // them filled).
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
@@ -40,15 +49,18 @@ namespace gi8 {
 
 constexpr int BK = 128;                 // bytes of K per stage: one swizzle row
 constexpr int UMMA_K = 32;              // K per tcgen05.mma kind::i8
-constexpr int CH = 128;                 // channels per CTA: the MMA's M side
-constexpr int MAX_T = 256;              // tokens per tile: the MMA's N side
+constexpr int CH = 128;                 // the MMA's M side in one CTA: channels (LARGE), tokens (STREAM)
+constexpr int MAX_N = 256;              // its N side: tokens (LARGE), channels (STREAM)
+constexpr int BLOCK = 32 * 33;          // STREAM: a 32 x 32 block of C on its way, rows padded by one
 constexpr int EPI_WARPS = 8;
 constexpr int EPI_THREADS = 32 * EPI_WARPS;
 constexpr int NUM_THREADS = 64 + EPI_THREADS;
 constexpr int SMEM_BUDGET = 226 * 1024;
-constexpr int MAX_STAGES = 12;
+constexpr int MAX_STAGES = 24;
 constexpr int MAX_K = 131071;           // 128 * 128 * K stays below 2^31
 constexpr int MAX_ROWS = 0x7fffff00;    // tile arithmetic stays in int
+
+enum { STREAM, LARGE, LARGE_PAIR };
 
 struct Params {
   int M, N;
@@ -58,11 +70,10 @@ struct Params {
   int t_rows;         // token rows this CTA loads (half of tt in a pair)
   int t_stage_bytes;  // stage bytes of the tokens
   int tmem_cols;      // two accumulators of half as many columns each
-  int stream;
-  int units;          // STREAM: 16-row units of channels
+  int height;         // channels of a tile that this CTA loads (LARGE: 128)
+  int c_stage_bytes;  // stage bytes of the channels
   int m_tiles;        // LARGE
   int tiles;
-  int heights[4];     // STREAM: the tile heights, one tensor map each
   int w_prefetch;     // K stages of B prefetched into L2 before the dependency wait
   const float* sa;
   const float* sb;
@@ -73,37 +84,43 @@ struct Params {
 
 struct Tile {
   int c0;      // this CTA's first channel
-  int c_rows;  // channels it loads (and the TMEM lanes that hold any)
   int m0;      // first token of the tile
 };
 
-// A CTA's range of n units is cut into this many tiles, the first n % tiles
-// of them one unit higher than the rest.
-__host__ __device__ inline int stream_tiles(int n) { return (n + CH / 16 - 1) / (CH / 16); }
-
+// Tile i.
 template <bool PAIR>
-__device__ __forceinline__ bool get_tile(const Params& p, int k, uint32_t rank, Tile& t) {
-  if (!PAIR && p.stream) {
-    const long long G = gridDim.x, c = blockIdx.x;
-    const int u0 = static_cast<int>(c * p.units / G);
-    const int n = static_cast<int>((c + 1) * p.units / G) - u0;
-    const int kt = stream_tiles(n);
-    if (k >= kt) return false;
-    const int h = n / kt, r = n - h * kt;
-    t.c0 = 16 * (u0 + k * h + min(k, r));
-    t.c_rows = 16 * (h + (k < r ? 1 : 0));
-    t.m0 = 0;
-    return true;
-  }
-  const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
-  const int count = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
-  const long long i = unit + static_cast<long long>(k) * count;
-  if (i >= p.tiles) return false;
-  const int ct = static_cast<int>(i) / p.m_tiles;
-  t.m0 = (static_cast<int>(i) - ct * p.m_tiles) * p.tt;
-  t.c0 = ct * (PAIR ? 2 * CH : CH) + static_cast<int>(rank) * CH;
-  t.c_rows = CH;
-  return true;
+__device__ __forceinline__ Tile tile_at(const Params& p, int i, uint32_t rank) {
+  Tile t;
+  const int ct = i / p.m_tiles;
+  t.m0 = (i - ct * p.m_tiles) * p.tt;
+  t.c0 = (PAIR ? 2 * ct + static_cast<int>(rank) : ct) * p.height;
+  return t;
+}
+
+// Ask for the tile of a CTA of this grid that has not started; 16 bytes of
+// answer arrive at `answer`, counted on `bar`.
+__device__ __forceinline__ void ask_tile(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+               "r"(bar)
+               : "memory");
+}
+
+// The tile in an answer that has arrived, -1 if there was none left.
+__device__ __forceinline__ int answered_tile(uint32_t answer) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(answer)
+      : "memory");
+  // the answer's bytes may be written again by the asynchronous proxy
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  return got ? static_cast<int>(x) : -1;
 }
 
 // Instruction descriptor of kind::i8: [4,6) D format (2 = s32); [7,10) and
@@ -133,21 +150,36 @@ __device__ __forceinline__ void umma_s8(uint32_t d_tmem, uint64_t adesc, uint64_
         : "memory");
 }
 
+__device__ __forceinline__ void load16(uint32_t taddr, int (&v)[16]) {
+  float f[16];
+  tmem_ld16(taddr, f);
+  tmem_ld_wait();
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = __float_as_int(f[j]);
+}
+
+__device__ __forceinline__ void load32(uint32_t taddr, int (&v)[32]) {
+  float f[2][16];
+  tmem_ld16(taddr, f[0]);
+  tmem_ld16(taddr + 16, f[1]);
+  tmem_ld_wait();
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = __float_as_int(f[j / 16][j % 16]);
+}
+
 __device__ __forceinline__ void put(float* c, float v) { *c = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* c, float v) { *c = __float2bfloat16_rn(v); }
 
-template <bool PAIR, typename OUT>
+template <int MODE, typename OUT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
-    gemm_i8_kernel(const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_c0,
-                   const __grid_constant__ CUtensorMap tm_c1, const __grid_constant__ CUtensorMap tm_c2,
-                   const __grid_constant__ CUtensorMap tm_c3, const Params p) {
+    gemm_i8_kernel(const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_c, const Params p) {
+  constexpr bool PAIR = MODE == LARGE_PAIR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  constexpr int C_STAGE = CH * BK;
-  const uint32_t s_c = smem_addr(smem);                                   // channels' stages
-  const uint32_t s_t = s_c + static_cast<uint32_t>(p.stages) * C_STAGE;   // tokens' stages
-  uint8_t* tail = smem + static_cast<size_t>(p.stages) * (C_STAGE + p.t_stage_bytes);
+  const uint32_t s_t = smem_addr(smem);                                           // tokens' stages
+  const uint32_t s_c = s_t + static_cast<uint32_t>(p.stages) * p.t_stage_bytes;   // channels' stages
+  uint8_t* tail = smem + static_cast<size_t>(p.stages) * (p.c_stage_bytes + p.t_stage_bytes);
   const uint32_t bar0 = smem_addr(tail);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (p.stages + s); };
@@ -155,7 +187,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * p.stages + 2 + b); };
   const uint32_t drain_bar = bar0 + 8u * (2 * p.stages + 4);
   const uint32_t handover_bar = bar0 + 8u * (2 * p.stages + 5);   // pair: the other CTA's count of loads
-  uint8_t* misc = tail + 8 * (2 * p.stages + 6);
+  // STREAM: two answers in turn, one barrier each for "arrived" and "read by all"
+  auto asked_bar = [&](int b) { return bar0 + 8u * (2 * p.stages + 6 + b); };
+  auto read_bar = [&](int b) { return bar0 + 8u * (2 * p.stages + 8 + b); };
+  __shared__ alignas(16) uint4 answers[2];
+  uint8_t* misc = tail + 8 * (2 * p.stages + 10);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   volatile int* peer_issued = reinterpret_cast<volatile int*>(misc + 8);
@@ -177,13 +213,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     mbar_init(drain_bar, 1);
     mbar_init(handover_bar, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(asked_bar(b), 1);
+      mbar_init(read_bar(b), 1 + EPI_WARPS);   // the issuer and the epilogue's warps
+    }
     *abort_flag = 0;
     *peer_issued = 0;
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tm_t);
-    prefetch_tmap(&tm_c0);
+    prefetch_tmap(&tm_c);
   }
   if (warp == 1) {
     if (PAIR)
@@ -198,26 +238,35 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int tmem_stride = p.tmem_cols >> 1;
-  auto channel_map = [&](int rows) {
-    return rows == p.heights[1] ? &tm_c1 : rows == p.heights[2] ? &tm_c2 : rows == p.heights[3] ? &tm_c3 : &tm_c0;
-  };
+  const int first_tile = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
   if (warp == 0 && lane == 0) {
     // B is a weight: its first stages may come into L2 while the kernel before
     // this one ends (L2 is the point of coherence, so nothing stale is seen
     // should that kernel write it after all)
-    Tile t;
-    if (get_tile<PAIR>(p, 0, rank, t)) {
-      const CUtensorMap* mc = channel_map(t.c_rows);
-      for (int kc = 0; kc < p.w_prefetch && kc < p.num_kc; ++kc) tma_prefetch_l2_2d(mc, kc * BK, t.c0);
-    }
+    const Tile t = tile_at<PAIR>(p, first_tile, rank);
+    for (int kc = 0; kc < p.w_prefetch && kc < p.num_kc; ++kc) tma_prefetch_l2_2d(&tm_c, kc * BK, t.c0);
   }
   pdl_wait();
   const uint64_t deadline = globaltimer_ns() + p.timeout_ns;
 
+  // The tile after `i`, the it-th of this CTA; -1 at the end, or when a wait
+  // gives up.  By one thread of each role.
+  auto next_tile = [&](int i, int it, bool counted) {
+    if (MODE != STREAM) {
+      const int step = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
+      return i < p.tiles - step ? i + step : -1;
+    }
+    if (!mbar_wait(asked_bar(it & 1), (it >> 1) & 1, deadline, abort_flag, p.status, peer_abort)) return -1;
+    const int n = answered_tile(smem_addr(answers + (it & 1)));
+    if (counted) mbar_arrive(read_bar(it & 1));
+    return n;
+  };
+
   int issued = 0;   // producer: stage loads issued, in ring order
+  int asked = 0;    // producer: tiles asked for
   if (warp == 0) {
     if (lane == 0) {
-      const uint64_t pol_c = p.stream ? l2_policy_evict_first() : l2_policy_evict_normal();
+      const uint64_t pol_c = MODE == STREAM ? l2_policy_evict_first() : l2_policy_evict_normal();
       const uint64_t pol_t = l2_policy_evict_last();
       int s = 0;
       uint32_t ph = 0;
@@ -228,11 +277,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         else
           tma_load_2d_hint(dst, m, fb, x, y, pol);
       };
-      Tile t;
-      for (int k = 0; ok && get_tile<PAIR>(p, k, rank, t); ++k) {
-        const CUtensorMap* mc = channel_map(t.c_rows);
+      for (int i = first_tile, it = 0; ok && i >= 0; i = ok ? next_tile(i, it, false) : -1, ++it) {
+        if (MODE == STREAM) {   // the tile after this one, while this one loads
+          if (it >= 2 && !mbar_wait(read_bar(it & 1), ((it >> 1) - 1) & 1, deadline, abort_flag, p.status, peer_abort)) break;
+          mbar_arrive_expect_tx(asked_bar(it & 1), 16);
+          ask_tile(smem_addr(answers + (it & 1)), asked_bar(it & 1));
+          ++asked;
+        }
+        const Tile t = tile_at<PAIR>(p, i, rank);
         const int t0 = t.m0 + static_cast<int>(rank) * p.t_rows;
-        const uint32_t tx = static_cast<uint32_t>((PAIR ? 2 : 1) * (t.c_rows + p.t_rows) * BK);
+        const uint32_t tx = static_cast<uint32_t>((PAIR ? 2 : 1) * (p.height + p.t_rows) * BK);
         for (int kc = 0; kc < p.num_kc; ++kc) {
           if (!mbar_wait(empty_bar(s), ph ^ 1u, deadline, abort_flag, p.status, peer_abort)) {
             ok = false;
@@ -240,7 +294,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           const uint32_t fb = full_bar(s);
           if (leader) mbar_arrive_expect_tx(fb, tx);
-          load(s_c + s * C_STAGE, mc, fb, kc * BK, t.c0, pol_c);
+          load(s_c + s * p.c_stage_bytes, &tm_c, fb, kc * BK, t.c0, pol_c);
           load(s_t + s * p.t_stage_bytes, &tm_t, fb, kc * BK, t0, pol_t);
           ++issued;
           if (++s == p.stages) {
@@ -256,7 +310,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
-      const uint32_t idesc = umma_idesc_s8(PAIR ? 2 * CH : CH, p.tt);
+      const uint32_t idesc = umma_idesc_s8(PAIR ? 2 * CH : CH, MODE == STREAM ? p.height : p.tt);
       int s = 0, tb = 0;
       uint32_t ph = 0, tph = 0;
       bool ok = true;
@@ -266,8 +320,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         else
           umma_commit(bar);
       };
-      Tile t;
-      for (int k = 0; ok && get_tile<PAIR>(p, k, rank, t); ++k) {
+      for (int i = first_tile, it = 0; ok && i >= 0; i = ok ? next_tile(i, it, true) : -1, ++it) {
         if (!mbar_wait(tempty_bar(tb), tph ^ 1u, deadline, abort_flag, p.status, peer_abort)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(tb * tmem_stride);
@@ -277,11 +330,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             break;
           }
           tc_fence_after();
-          const uint64_t cdesc = umma_desc_sw128(s_c + s * C_STAGE);
+          const uint64_t cdesc = umma_desc_sw128(s_c + s * p.c_stage_bytes);
           const uint64_t tdesc = umma_desc_sw128(s_t + s * p.t_stage_bytes);
+          const uint64_t mdesc = MODE == STREAM ? tdesc : cdesc, ndesc = MODE == STREAM ? cdesc : tdesc;
 #pragma unroll
           for (int kk = 0; kk < BK / UMMA_K; ++kk)   // 32 bytes of K on: the address field counts 16
-            umma_s8<PAIR>(d_tmem, cdesc + 2ull * kk, tdesc + 2ull * kk, idesc, (kc | kk) != 0 ? 1u : 0u);
+            umma_s8<PAIR>(d_tmem, mdesc + 2ull * kk, ndesc + 2ull * kk, idesc, (kc | kk) != 0 ? 1u : 0u);
           commit(empty_bar(s));
           if (++s == p.stages) {
             s = 0;
@@ -308,34 +362,56 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int quarter = warp & 3;             // the TMEM lanes this warp may access
     const int half = (warp - 2) >> 2;         // which half of the tile's tokens
     const int nch = p.tt / 16, split = (nch + 1) >> 1;
+    float* block = reinterpret_cast<float*>(tail + 8 * (2 * p.stages + 10) + 16) + (quarter * 2 + half) * BLOCK;
+    const float sa_row = MODE == STREAM && quarter * 32 + lane < p.M ? __ldg(p.sa + quarter * 32 + lane) : 0.f;
     int tb = 0;
     uint32_t tph = 0;
-    Tile t;
-    for (int k = 0; get_tile<PAIR>(p, k, rank, t); ++k) {
+    for (int i = first_tile, it = 0; i >= 0; ++it) {
+      const Tile t = tile_at<PAIR>(p, i, rank);
       int ok = 0;
       if (lane == 0) ok = mbar_wait(tfull_bar(tb), tph, deadline, abort_flag, p.status, peer_abort) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after();
-      const int n = t.c0 + quarter * 32 + lane;
-      const bool mine = quarter * 32 + lane < t.c_rows && n < p.N;
-      const float sbn = mine ? __ldg(p.sb + n) : 0.f;
       const uint32_t taddr =
           tmem_base + static_cast<uint32_t>(tb * tmem_stride) + (static_cast<uint32_t>(quarter * 32) << 16);
-      const int ch_end = __any_sync(0xffffffffu, mine) ? (half ? nch : split) : 0;
-      for (int ch = half ? split : 0; ch < ch_end; ++ch) {
-        const int m = t.m0 + ch * 16;
-        if (m >= p.M) break;
-        float x[16];
-        tmem_ld16(taddr + ch * 16, x);
-        tmem_ld_wait();
-        OUT* c = static_cast<OUT*>(p.C) + static_cast<size_t>(m) * p.N + n;
-        const int rows = min(16, p.M - m);
-        if (mine) {
+      if constexpr (MODE == STREAM) {
+        // blocks of 32 tokens (this warp's lanes) x 32 channels; the two warps
+        // of a quarter take every other block
+        const int m0 = quarter * 32, rows = min(32, p.M - m0);
+        for (int b = half; rows > 0 && b * 32 < p.height && t.c0 + b * 32 < p.N; b += 2) {
+          int x[32];
+          load32(taddr + b * 32, x);
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (j < rows)
-              put(c + static_cast<size_t>(j) * p.N, __int2float_rn(__float_as_int(x[j])) * __ldg(p.sa + m + j) * sbn);
+          for (int j = 0; j < 32; ++j) block[lane * 33 + j] = __int2float_rn(x[j]) * sa_row;
+          __syncwarp();
+          const int n = t.c0 + b * 32 + lane;
+          if (b * 32 + lane < p.height && n < p.N) {
+            const float sbn = __ldg(p.sb + n);
+            OUT* c = static_cast<OUT*>(p.C) + static_cast<size_t>(m0) * p.N + n;
+#pragma unroll 8
+            for (int r = 0; r < rows; ++r) put(c + static_cast<size_t>(r) * p.N, block[r * 33 + lane] * sbn);
+          }
+          __syncwarp();
+        }
+      } else {
+        const int n = t.c0 + quarter * 32 + lane;
+        const bool mine = quarter * 32 + lane < p.height && n < p.N;
+        const float sbn = mine ? __ldg(p.sb + n) : 0.f;
+        const int ch_end = __any_sync(0xffffffffu, mine) ? (half ? nch : split) : 0;
+        for (int ch = half ? split : 0; ch < ch_end; ++ch) {
+          const int m = t.m0 + ch * 16;
+          if (m >= p.M) break;
+          int x[16];
+          load16(taddr + ch * 16, x);
+          OUT* c = static_cast<OUT*>(p.C) + static_cast<size_t>(m) * p.N + n;
+          const int rows = min(16, p.M - m);
+          if (mine) {
+  #pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (j < rows)
+                put(c + static_cast<size_t>(j) * p.N, __int2float_rn(x[j]) * __ldg(p.sa + m + j) * sbn);
+          }
         }
       }
       tc_fence_before();
@@ -347,6 +423,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tb = 0;
         tph ^= 1u;
       }
+      if (lane == 0) i = next_tile(i, it, true);
+      i = __shfl_sync(0xffffffffu, i, 0);
     }
   }
 
@@ -379,6 +457,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       while (!mbar_try_wait(full_bar(q), par) && globaltimer_ns() < dl) {
       }
     }
+    for (int it = max(asked - 2, 0); it < asked; ++it)
+      while (!mbar_try_wait(asked_bar(it & 1), (it >> 1) & 1) && globaltimer_ns() < dl) {
+      }
   }
   if (PAIR) {
     __syncwarp();
@@ -409,14 +490,10 @@ static bool make_map(CUtensorMap* m, const void* base, int rows, int cols, int b
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-static size_t smem_bytes(const Params& p) {
-  return 1024 + static_cast<size_t>(p.stages) * (CH * BK + p.t_stage_bytes) + 8 * (2 * p.stages + 6) + 16;
-}
-
 // At every launch: the attribute belongs to the current device and context.
-template <bool PAIR, typename OUT>
+template <int MODE, typename OUT>
 static cudaError_t allow_smem() {
-  return cudaFuncSetAttribute(gemm_i8_kernel<PAIR, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BUDGET);
+  return cudaFuncSetAttribute(gemm_i8_kernel<MODE, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BUDGET);
 }
 
 // Clusters of two that can be resident at once on the current device (0:
@@ -430,7 +507,7 @@ static int max_pairs() {
     const int k = known[dev].load(std::memory_order_relaxed);
     if (k > 0) return k - 1;
   }
-  if (allow_smem<true, float>() != cudaSuccess) return 0;
+  if (allow_smem<LARGE_PAIR, float>() != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(NUM_THREADS);
@@ -443,7 +520,7 @@ static int max_pairs() {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int c = 0;
-  if (cudaOccupancyMaxActiveClusters(&c, gemm_i8_kernel<true, float>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&c, gemm_i8_kernel<LARGE_PAIR, float>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -453,9 +530,20 @@ static int max_pairs() {
 
 struct Plan {
   Params p;
-  bool pair;
+  int mode;
   int grid;
 };
+
+// STREAM: an MMA reads 128 rows from its token stage's start.  What lies past
+// the stage is never read back, but has to be shared memory of the CTA: the
+// span of the last stage ends inside the ring or what follows it.
+static size_t smem_bytes(const Plan& pl) {
+  const Params& p = pl.p;
+  const size_t ring = static_cast<size_t>(p.stages) * (p.c_stage_bytes + p.t_stage_bytes);
+  const size_t span = static_cast<size_t>(p.stages - 1) * p.t_stage_bytes + CH * BK;
+  const size_t blocks = pl.mode == STREAM ? sizeof(float) * BLOCK * 2 * ((p.M + 31) / 32) : 0;
+  return 1024 + std::max(ring + 8 * (2 * p.stages + 10) + 16 + blocks, span);
+}
 
 static bool make_plan(int M, int N, int K, int sms, Plan& pl) {
   Params& p = pl.p;
@@ -463,34 +551,33 @@ static bool make_plan(int M, int N, int K, int sms, Plan& pl) {
   p.M = M;
   p.N = N;
   p.num_kc = (K + BK - 1) / BK;
-  pl.pair = false;
   if (M <= CH) {
-    p.stream = 1;
+    pl.mode = STREAM;
     p.tt = (M + 15) & ~15;
     p.t_rows = p.tt;
-    p.units = (N + 15) / 16;
-    pl.grid = p.units < sms ? p.units : sms;
-    // a range has u or u + 1 units and tiles of two heights: at most four
-    const int u = p.units / pl.grid;
-    int k = 0;
-    for (int n = u; n <= u + 1; ++n) {
-      const int kt = stream_tiles(n);
-      for (int h : {n / kt, n / kt + (n % kt ? 1 : 0)}) {
-        bool have = false;
-        for (int j = 0; j < k; ++j) have = have || p.heights[j] == 16 * h;
-        if (!have) p.heights[k++] = 16 * h;
-      }
-    }
+    const int units = (N + 15) / 16;
+    // the highest tiles of which every SM gets the same number: fewer tiles
+    // are fewer MMAs, and less is read of the tokens for each ([8 x 151936 x
+    // 2560]: 13 units high 66 us, 16 units, four for each SM and two left over,
+    // 70; 8 units 77)
+    const int rounds = (units + MAX_N / 16 * sms - 1) / (MAX_N / 16 * sms);
+    const int h = (units + rounds * sms - 1) / (rounds * sms);
+    p.height = 16 * h;
+    p.m_tiles = 1;
+    p.tiles = pl.grid = (units + h - 1) / h;
   } else {
     const int pairs = pair_allowed() ? max_pairs() : 0;
-    pl.pair = pairs >= 1;
-    const int units = pl.pair ? (pairs < sms / 2 ? pairs : sms / 2) : sms;
-    const int ch = pl.pair ? 2 * CH : CH;
+    const bool pair = pairs >= 1;
+    pl.mode = pair ? LARGE_PAIR : LARGE;
+    const int units = pair ? (pairs < sms / 2 ? pairs : sms / 2) : sms;
+    const int ch = pair ? 2 * CH : CH;
     const long long c_tiles = (static_cast<long long>(N) + ch - 1) / ch;
     // tokens per tile: the fewest rounds of tiles, a tile's time being that
-    // of its operands' bytes (channels plus tokens)
+    // of its operands' bytes, which come at 57 B/ns to an SM (channels plus
+    // tokens; [448 x 151936 x 2560]: 6.8, 8.3, 9.5 and 11.6 us a tile of 64,
+    // 128, 192 and 256)
     long long best = -1;
-    for (int tt = MAX_T; tt >= 32; tt -= 32) {
+    for (int tt = MAX_N; tt >= 32; tt -= 32) {
       const long long tiles = c_tiles * ((M + tt - 1) / tt);
       const long long cost = (tiles + units - 1) / units * (ch + tt);
       if (best < 0 || cost < best) {
@@ -502,24 +589,26 @@ static bool make_plan(int M, int N, int K, int sms, Plan& pl) {
     const long long tiles = c_tiles * p.m_tiles;
     if (tiles > 0x7fffffffLL) return false;
     p.tiles = static_cast<int>(tiles);
-    p.t_rows = pl.pair ? p.tt / 2 : p.tt;
-    p.heights[0] = CH;
+    p.t_rows = pair ? p.tt / 2 : p.tt;
+    p.height = CH;
     const int used = tiles < units ? static_cast<int>(tiles) : units;
-    pl.grid = pl.pair ? 2 * used : used;
+    pl.grid = pair ? 2 * used : used;
   }
   p.t_stage_bytes = p.t_rows * BK;
+  p.c_stage_bytes = p.height * BK;
   p.tmem_cols = 32;
-  while (p.tmem_cols < 2 * p.tt) p.tmem_cols *= 2;
-  for (p.stages = MAX_STAGES; p.stages > 2 && smem_bytes(p) > SMEM_BUDGET;) --p.stages;
-  return smem_bytes(p) <= SMEM_BUDGET;
+  const int columns = pl.mode == STREAM ? (p.height + 31) & ~31 : p.tt;   // read in blocks of 32 (STREAM) or 16
+  while (p.tmem_cols < 2 * columns) p.tmem_cols *= 2;
+  for (p.stages = MAX_STAGES; p.stages > 2 && smem_bytes(pl) > SMEM_BUDGET;) --p.stages;
+  return smem_bytes(pl) <= SMEM_BUDGET;
 }
 
-template <bool PAIR, typename OUT>
-static cudaError_t launch_as(const Plan& pl, const CUtensorMap& tt, const CUtensorMap* tc, cudaStream_t st) {
-  const cudaError_t e = allow_smem<PAIR, OUT>();
+template <int MODE, typename OUT>
+static cudaError_t launch_as(const Plan& pl, const CUtensorMap& tt, const CUtensorMap& tc, cudaStream_t st) {
+  const cudaError_t e = allow_smem<MODE, OUT>();
   if (e != cudaSuccess) return e;
-  return launch_kernel_cluster(gemm_i8_kernel<PAIR, OUT>, dim3(pl.grid), dim3(NUM_THREADS), smem_bytes(pl.p), st,
-                               PAIR ? 2 : 1, tt, tc[0], tc[1], tc[2], tc[3], pl.p);
+  return launch_kernel_cluster(gemm_i8_kernel<MODE, OUT>, dim3(pl.grid), dim3(NUM_THREADS), smem_bytes(pl), st,
+                               MODE == LARGE_PAIR ? 2 : 1, tt, tc, pl.p);
 }
 
 }  // namespace gi8
@@ -539,26 +628,22 @@ extern "C" int dflash_gemm_i8(const int8_t* A, const float* sa, const int8_t* B,
   Plan pl;
   if (!make_plan(M, N, K, sms, pl)) return DFLASH_ERR_UNSUPPORTED;
   Params& p = pl.p;
-  p.w_prefetch = p.stream ? 8 : 0;
+  p.w_prefetch = pl.mode == STREAM ? 8 : 0;
   p.sa = sa;
   p.sb = sb;
   p.C = C;
   p.status = dev_status;
   p.timeout_ns = timeout_ns_from_env();
-  CUtensorMap tt, tc[4];
-  bool ok = gi8::make_map(&tt, A, M, K, p.t_rows);
-  for (int j = 0; j < 4; ++j) {
-    if (p.heights[j] > 0)
-      ok = ok && gi8::make_map(&tc[j], B, N, K, p.heights[j]);
-    else
-      tc[j] = tc[0];
-  }
+  CUtensorMap tt, tc;
+  const bool ok = gi8::make_map(&tt, A, M, K, p.t_rows) && gi8::make_map(&tc, B, N, K, p.height);
   if (!ok) return DFLASH_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (pl.pair)
-    e = c_bf16 ? launch_as<true, __nv_bfloat16>(pl, tt, tc, st) : launch_as<true, float>(pl, tt, tc, st);
+  if (pl.mode == STREAM)
+    e = c_bf16 ? launch_as<STREAM, __nv_bfloat16>(pl, tt, tc, st) : launch_as<STREAM, float>(pl, tt, tc, st);
+  else if (pl.mode == LARGE_PAIR)
+    e = c_bf16 ? launch_as<LARGE_PAIR, __nv_bfloat16>(pl, tt, tc, st) : launch_as<LARGE_PAIR, float>(pl, tt, tc, st);
   else
-    e = c_bf16 ? launch_as<false, __nv_bfloat16>(pl, tt, tc, st) : launch_as<false, float>(pl, tt, tc, st);
+    e = c_bf16 ? launch_as<LARGE, __nv_bfloat16>(pl, tt, tc, st) : launch_as<LARGE, float>(pl, tt, tc, st);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }

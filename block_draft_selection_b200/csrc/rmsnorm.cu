@@ -254,7 +254,7 @@ static int launch(const Args& a, int M, cudaStream_t st) {
     e = launch_as<4, 1024, 1, NORM, I8>(a, M, st);
   else if (M <= num_sms_current())
     e = launch_as<1, 1024, 1, NORM, I8>(a, M, st);
-  else if (NORM)
+  else if constexpr (NORM)
     e = launch_as<2, 512, 3, NORM, I8>(a, M, st);
   else
     e = launch_as<4, 256, 5, NORM, I8>(a, M, st);
