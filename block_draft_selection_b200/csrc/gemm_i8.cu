@@ -8,14 +8,14 @@
 //   warp 1      MMA issuer into a double-buffered TMEM accumulator; owns the
 //               TMEM allocation
 //   warps 2..9  epilogue: TMEM -> registers -> C
-// A tcgen05.mma of M = 128 takes about 150 clocks whatever its N up to 128 or
-// so (measured: 600 a stage of four, on one accumulator or on four in turn), so
-// the operand whose bytes bound the call goes where an instruction takes more
-// of it, the N side:
+// A stage costs the lanes that issue for it 350 to 450 clocks whatever it
+// holds, and an SM's share of the memory bandwidth is about 23 bytes a clock, so
+// stages are kept full, with the operand whose bytes bound the call on the side
+// of the MMA that takes more of it:
 //   STREAM (M <= 128, bound by the bytes of B): channels (rows of B) on the N
 //          side, up to 256 a tile, the tokens (rows of A), rounded up to 16, on
-//          the M side.  (With the channels on the M side a stage of 16 KB took
-//          its 600 clocks, just the SM's share of the memory bandwidth.)  The
+//          the M side: a stage holds up to 32 KB of B (with the channels on the
+//          M side 16 KB; [96 x 151936 x 5120] took 159 us, so it took 147).  The
 //          tiles are dealt out as CTAs come to need them, since SMs do not get
 //          equal shares of the bandwidth: the grid has a CTA per tile, the
 //          first ones run, and each asks the hardware to cancel a CTA that has
@@ -150,12 +150,28 @@ __device__ __forceinline__ void umma_s8(uint32_t d_tmem, uint64_t adesc, uint64_
         : "memory");
 }
 
-__device__ __forceinline__ void load16(uint32_t taddr, int (&v)[16]) {
-  float f[16];
-  tmem_ld16(taddr, f);
-  tmem_ld_wait();
-#pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = __float_as_int(f[j]);
+// Whether the phase is complete, at once (mbarrier.try_wait may wait a while).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// True in one lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ void load32(uint32_t taddr, int (&v)[32]) {
@@ -249,71 +265,97 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   pdl_wait();
   const uint64_t deadline = globaltimer_ns() + p.timeout_ns;
 
-  // The tile after `i`, the it-th of this CTA; -1 at the end, or when a wait
-  // gives up.  By one thread of each role.
+  // The producer's and the issuer's loops are run by their whole warps, and one
+  // lane issues: addresses, coordinates and descriptors then are in uniform
+  // registers, where these instructions take them from, and each looks at the
+  // next stage's barrier before it issues for this one (a barrier that is
+  // complete still takes 160 clocks to be seen).  With the loops inside a branch
+  // for one lane a stage took its producer 500 clocks and its issuer 710, which
+  // bound every size.
+  const bool elected = elect_one();
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    bool ok = true;
+    while (ok && !mbar_try_wait(bar, parity)) {
+      if (*abort_flag) {
+        ok = false;
+      } else if (globaltimer_ns() > deadline) {   // both CTAs of a pair stop together
+        ok = false;
+        set_status(p.status, DFLASH_ERR_TIMEOUT);
+        *abort_flag = 1;
+        if (PAIR) st_shared_cluster_u32(peer_abort, 1u);
+      }
+    }
+    return __all_sync(0xffffffffu, ok) != 0;
+  };
+  // The tile after `i`, the it-th of this CTA, in all lanes of a warp; -1 at
+  // the end, or when a wait gives up.
   auto next_tile = [&](int i, int it, bool counted) {
     if (MODE != STREAM) {
       const int step = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
       return i < p.tiles - step ? i + step : -1;
     }
-    if (!mbar_wait(asked_bar(it & 1), (it >> 1) & 1, deadline, abort_flag, p.status, peer_abort)) return -1;
-    const int n = answered_tile(smem_addr(answers + (it & 1)));
-    if (counted) mbar_arrive(read_bar(it & 1));
+    if (!wait(asked_bar(it & 1), (it >> 1) & 1)) return -1;
+    const int n = __reduce_max_sync(0xffffffffu, answered_tile(smem_addr(answers + (it & 1))));
+    if (counted && elected) mbar_arrive(read_bar(it & 1));
     return n;
   };
 
   int issued = 0;   // producer: stage loads issued, in ring order
   int asked = 0;    // producer: tiles asked for
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol_c = MODE == STREAM ? l2_policy_evict_first() : l2_policy_evict_normal();
-      const uint64_t pol_t = l2_policy_evict_last();
-      int s = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t fb, int x, int y, uint64_t pol) {
-        if (PAIR)
-          tma_load_2d_pair(dst, m, mapa_shared(fb, 0), x, y, pol);
-        else
-          tma_load_2d_hint(dst, m, fb, x, y, pol);
-      };
-      for (int i = first_tile, it = 0; ok && i >= 0; i = ok ? next_tile(i, it, false) : -1, ++it) {
-        if (MODE == STREAM) {   // the tile after this one, while this one loads
-          if (it >= 2 && !mbar_wait(read_bar(it & 1), ((it >> 1) - 1) & 1, deadline, abort_flag, p.status, peer_abort)) break;
+    const uint64_t pol_c = MODE == STREAM ? l2_policy_evict_first() : l2_policy_evict_normal();
+    const uint64_t pol_t = l2_policy_evict_last();
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true, ready = true;   // ready: the stage's barrier has been seen to be complete
+    auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t fb, int x, int y, uint64_t pol) {
+      if (PAIR)
+        tma_load_2d_pair(dst, m, mapa_shared(fb, 0), x, y, pol);
+      else
+        tma_load_2d_hint(dst, m, fb, x, y, pol);
+    };
+    const uint32_t tx = static_cast<uint32_t>((PAIR ? 2 : 1) * (p.height + p.t_rows) * BK);
+    for (int i = first_tile, it = 0; ok && i >= 0; i = ok ? next_tile(i, it, false) : -1, ++it) {
+      if (MODE == STREAM) {   // the tile after this one, while this one loads
+        if (it >= 2 && !wait(read_bar(it & 1), ((it >> 1) - 1) & 1)) break;
+        if (elected) {
           mbar_arrive_expect_tx(asked_bar(it & 1), 16);
           ask_tile(smem_addr(answers + (it & 1)), asked_bar(it & 1));
-          ++asked;
         }
-        const Tile t = tile_at<PAIR>(p, i, rank);
-        const int t0 = t.m0 + static_cast<int>(rank) * p.t_rows;
-        const uint32_t tx = static_cast<uint32_t>((PAIR ? 2 : 1) * (p.height + p.t_rows) * BK);
-        for (int kc = 0; kc < p.num_kc; ++kc) {
-          if (!mbar_wait(empty_bar(s), ph ^ 1u, deadline, abort_flag, p.status, peer_abort)) {
-            ok = false;
-            break;
-          }
-          const uint32_t fb = full_bar(s);
-          if (leader) mbar_arrive_expect_tx(fb, tx);
-          load(s_c + s * p.c_stage_bytes, &tm_c, fb, kc * BK, t.c0, pol_c);
-          load(s_t + s * p.t_stage_bytes, &tm_t, fb, kc * BK, t0, pol_t);
-          ++issued;
-          if (++s == p.stages) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
+        ++asked;
       }
-      if (PAIR && !leader) {
-        st_shared_cluster_u32(mapa_shared(smem_addr(const_cast<int*>(peer_issued)), 0), static_cast<uint32_t>(issued));
-        mbar_arrive_cluster(mapa_shared(handover_bar, 0));   // release: the count is visible first
+      const Tile t = tile_at<PAIR>(p, i, rank);
+      const int t0 = t.m0 + static_cast<int>(rank) * p.t_rows;
+      for (int kc = 0; kc < p.num_kc; ++kc) {
+        if (!ready && !wait(empty_bar(s), ph ^ 1u)) {
+          ok = false;
+          break;
+        }
+        const int s1 = s + 1 == p.stages ? 0 : s + 1;
+        const uint32_t ph1 = s1 == 0 ? ph ^ 1u : ph;
+        const bool peek = mbar_test(empty_bar(s1), ph1 ^ 1u);
+        const uint32_t fb = full_bar(s), to_c = s_c + s * p.c_stage_bytes, to_t = s_t + s * p.t_stage_bytes;
+        if (elected) {
+          if (leader) mbar_arrive_expect_tx(fb, tx);
+          load(to_c, &tm_c, fb, kc * BK, t.c0, pol_c);
+          load(to_t, &tm_t, fb, kc * BK, t0, pol_t);
+        }
+        ++issued;
+        ready = __all_sync(0xffffffffu, peek) != 0;
+        s = s1;
+        ph = ph1;
       }
     }
+    if (PAIR && !leader && elected) {
+      st_shared_cluster_u32(mapa_shared(smem_addr(const_cast<int*>(peer_issued)), 0), static_cast<uint32_t>(issued));
+      mbar_arrive_cluster(mapa_shared(handover_bar, 0));   // release: the count is visible first
+    }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       const uint32_t idesc = umma_idesc_s8(PAIR ? 2 * CH : CH, MODE == STREAM ? p.height : p.tt);
       int s = 0, tb = 0;
       uint32_t ph = 0, tph = 0;
-      bool ok = true;
+      bool ok = true, ready = false;
       auto commit = [&](uint32_t bar) {
         if (PAIR)
           umma_commit_pair_multicast(bar, 0x3);
@@ -321,39 +363,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           umma_commit(bar);
       };
       for (int i = first_tile, it = 0; ok && i >= 0; i = ok ? next_tile(i, it, true) : -1, ++it) {
-        if (!mbar_wait(tempty_bar(tb), tph ^ 1u, deadline, abort_flag, p.status, peer_abort)) break;
+        if (!wait(tempty_bar(tb), tph ^ 1u)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(tb * tmem_stride);
         for (int kc = 0; kc < p.num_kc; ++kc) {
-          if (!mbar_wait(full_bar(s), ph, deadline, abort_flag, p.status, peer_abort)) {
+          if (!ready && !wait(full_bar(s), ph)) {
             ok = false;
             break;
           }
+          const int s1 = s + 1 == p.stages ? 0 : s + 1;
+          const uint32_t ph1 = s1 == 0 ? ph ^ 1u : ph;
+          const bool peek = mbar_test(full_bar(s1), ph1);
           tc_fence_after();
           const uint64_t cdesc = umma_desc_sw128(s_c + s * p.c_stage_bytes);
           const uint64_t tdesc = umma_desc_sw128(s_t + s * p.t_stage_bytes);
           const uint64_t mdesc = MODE == STREAM ? tdesc : cdesc, ndesc = MODE == STREAM ? cdesc : tdesc;
+          const uint32_t eb = empty_bar(s);
+          if (elected) {
 #pragma unroll
-          for (int kk = 0; kk < BK / UMMA_K; ++kk)   // 32 bytes of K on: the address field counts 16
-            umma_s8<PAIR>(d_tmem, mdesc + 2ull * kk, ndesc + 2ull * kk, idesc, (kc | kk) != 0 ? 1u : 0u);
-          commit(empty_bar(s));
-          if (++s == p.stages) {
-            s = 0;
-            ph ^= 1u;
+            for (int kk = 0; kk < BK / UMMA_K; ++kk)   // 32 bytes of K on: the address field counts 16
+              umma_s8<PAIR>(d_tmem, mdesc + 2ull * kk, ndesc + 2ull * kk, idesc, (kc | kk) != 0 ? 1u : 0u);
+            commit(eb);
           }
+          ready = __all_sync(0xffffffffu, peek) != 0;
+          s = s1;
+          ph = ph1;
         }
         if (!ok) break;
-        commit(tfull_bar(tb));
+        if (elected) commit(tfull_bar(tb));
         if (++tb == 2) {
           tb = 0;
           tph ^= 1u;
         }
       }
       // every MMA issued has completed before TMEM is released
-      if (PAIR)
-        umma_commit_pair(drain_bar);
-      else
-        umma_commit(drain_bar);
+      if (elected) {
+        if (PAIR)
+          umma_commit_pair(drain_bar);
+        else
+          umma_commit(drain_bar);
+      }
       const uint64_t dl = globaltimer_ns() + 50000000ull;
       while (!mbar_try_wait(drain_bar, 0) && globaltimer_ns() < dl) {
       }
@@ -368,10 +417,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t tph = 0;
     for (int i = first_tile, it = 0; i >= 0; ++it) {
       const Tile t = tile_at<PAIR>(p, i, rank);
-      int ok = 0;
-      if (lane == 0) ok = mbar_wait(tfull_bar(tb), tph, deadline, abort_flag, p.status, peer_abort) ? 1 : 0;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
+      if (!wait(tfull_bar(tb), tph)) break;
       tc_fence_after();
       const uint32_t taddr =
           tmem_base + static_cast<uint32_t>(tb * tmem_stride) + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -399,18 +445,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const bool mine = quarter * 32 + lane < p.height && n < p.N;
         const float sbn = mine ? __ldg(p.sb + n) : 0.f;
         const int ch_end = __any_sync(0xffffffffu, mine) ? (half ? nch : split) : 0;
-        for (int ch = half ? split : 0; ch < ch_end; ++ch) {
+        for (int ch = half ? split : 0; ch < ch_end; ch += 2) {
           const int m = t.m0 + ch * 16;
           if (m >= p.M) break;
-          int x[16];
-          load16(taddr + ch * 16, x);
+          // two chunks of 16 tokens (one at the end), their scales a lane each
+          const int rows = min(p.M - m, 16 * min(2, ch_end - ch));
+          const float sam = lane < rows ? __ldg(p.sa + m + lane) : 0.f;
+          int x[32];
+          load32(taddr + ch * 16, x);
           OUT* c = static_cast<OUT*>(p.C) + static_cast<size_t>(m) * p.N + n;
-          const int rows = min(16, p.M - m);
-          if (mine) {
-  #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (j < rows)
-                put(c + static_cast<size_t>(j) * p.N, __int2float_rn(x[j]) * __ldg(p.sa + m + j) * sbn);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float v = __int2float_rn(x[j]) * __shfl_sync(0xffffffffu, sam, j) * sbn;
+            if (j < rows && mine) put(c, v);
+            c += p.N;
           }
         }
       }
@@ -423,8 +471,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tb = 0;
         tph ^= 1u;
       }
-      if (lane == 0) i = next_tile(i, it, true);
-      i = __shfl_sync(0xffffffffu, i, 0);
+      i = next_tile(i, it, true);
     }
   }
 
@@ -433,7 +480,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   __syncwarp();
   if (PAIR) cluster_sync_all();   // every role of both CTAs is done: abort flags and counts are final
-  if (warp == 0 && lane == 0 && leader && *abort_flag != 0) {
+  if (warp == 0 && elected && leader && *abort_flag != 0) {
     // Loads issued but never consumed must land before the CTA (and the other
     // CTA of a pair) may exit.  A stage load that only the leader issued has
     // the other CTA's bytes counted as arrived; one that only the other CTA
@@ -461,7 +508,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       while (!mbar_try_wait(asked_bar(it & 1), (it >> 1) & 1) && globaltimer_ns() < dl) {
       }
   }
-  if (PAIR) {
+  if (PAIR && *abort_flag != 0) {   // set in both CTAs or in neither
     __syncwarp();
     cluster_sync_all();   // the other CTA stays until the leader's drain is done
   }
@@ -597,7 +644,7 @@ static bool make_plan(int M, int N, int K, int sms, Plan& pl) {
   p.t_stage_bytes = p.t_rows * BK;
   p.c_stage_bytes = p.height * BK;
   p.tmem_cols = 32;
-  const int columns = pl.mode == STREAM ? (p.height + 31) & ~31 : p.tt;   // read in blocks of 32 (STREAM) or 16
+  const int columns = ((pl.mode == STREAM ? p.height : p.tt) + 31) & ~31;   // read in blocks of 32
   while (p.tmem_cols < 2 * columns) p.tmem_cols *= 2;
   for (p.stages = MAX_STAGES; p.stages > 2 && smem_bytes(pl) > SMEM_BUDGET;) --p.stages;
   return smem_bytes(pl) <= SMEM_BUDGET;
