@@ -263,7 +263,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int kc = 0; kc < p.w_prefetch && kc < p.num_kc; ++kc) tma_prefetch_l2_2d(&tm_c, kc * BK, t.c0);
   }
   pdl_wait();
-  const uint64_t deadline = globaltimer_ns() + p.timeout_ns;
 
   // The producer's and the issuer's loops are run by their whole warps, and one
   // lane issues: addresses, coordinates and descriptors then are in uniform
@@ -275,10 +274,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const bool elected = elect_one();
   auto wait = [&](uint32_t bar, uint32_t parity) {
     bool ok = true;
+    uint64_t deadline = 0;   // of this wait, from the first look that was in vain
     while (ok && !mbar_try_wait(bar, parity)) {
+      const uint64_t now = globaltimer_ns();
+      if (deadline == 0) deadline = now + p.timeout_ns;
       if (*abort_flag) {
         ok = false;
-      } else if (globaltimer_ns() > deadline) {   // both CTAs of a pair stop together
+      } else if (now > deadline) {   // both CTAs of a pair stop together
         ok = false;
         set_status(p.status, DFLASH_ERR_TIMEOUT);
         *abort_flag = 1;

@@ -487,12 +487,18 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
 #pragma unroll
     for (int r = 0; r < S - 1; ++r) fetch(r);
   }
-  if (!rt.asked(p, row)) {   // the same for every CTA of the cluster
-    copies_wait<0>();
-    return;
-  }
   // remote stores wait until every CTA of the cluster has started
   if (Q > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (!rt.asked(p, row)) {
+    copies_wait<0>();
+    // every CTA of the cluster comes to the same answer, unless the tokens
+    // change meanwhile; the barriers are met in that case too
+    if (Q > 1) {
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      cluster_sync_all();
+    }
+    return;
+  }
   if (!p.eager) {
 #pragma unroll
     for (int r = 0; r < S - 1; ++r) fetch(r);

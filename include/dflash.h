@@ -464,7 +464,8 @@ int dflash_gemm_i8(const int8_t* A, const float* sa, const int8_t* B, const floa
  * makes its lse, entropy and log-probabilities NaN; a NaN counts as the
  * largest value in top_idx.
  * tokens [M] int32: a negative one marks a row that is not asked for (padding
- * of a batch): it is not read, and its outputs keep what they held.  A token
+ * of a batch): its outputs keep what they held (its logits may be read, with
+ * no effect).  A token
  * >= V records DFLASH_ERR_BAD_INDEX; its row gets logp = NaN and rank = 0 and
  * the rest as usual.  tokens NULL: no tokens (every row is asked for; logp
  * and rank must be NULL).
@@ -485,7 +486,7 @@ int dflash_token_logprobs(const void* logits, int z_bf16, long long ld, int M, i
  * or bf16, or ld elements apart) with
  *   token = draft[b,i] for i < accept_len[b] - 1,
  *   token = next_token[b] for i = accept_len[b] - 1;
- * rows behind that are not read and their outputs keep what they held.
+ * the outputs of the rows behind that keep what they held.
  * draft [B, L], accept_len, next_token [B] int32 as dflash_verify and
  * dflash_verify_rejection give them; an accept_len outside [1, L+1] records
  * DFLASH_ERR_BAD_INDEX and is clamped; a token outside [0, V) records it too,

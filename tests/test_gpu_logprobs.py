@@ -181,6 +181,54 @@ def test_rows_not_asked_for_keep_what_they_held():
     assert not fresh[0][0] and not fresh[5][8].any()          # what the call allocates is zero there
 
 
+def test_padding_among_rows_that_clusters_share():
+    """Few long rows, several CTAs to each: rows not asked for leave their outputs alone."""
+    M, V, K = 6, 151936, 20
+    z, z64 = _logits(M, V, 21)
+    tok, _ = _tokens(M, V, 21)
+    tok[[0, 3, 5]] = -1
+    top = torch.full((M, K), 7, dtype=torch.int32, device="cuda")
+    for _ in range(3):
+        out, status = _call(z, torch.from_numpy(tok).cuda(), K, top_idx=top)
+        assert status == 0 and (top[[0, 3, 5]] == 7).all()
+        keep = tok >= 0
+        ref = oracle.token_logprobs(z64[keep], tok[keep], 1.0, K)
+        _compare([t[torch.from_numpy(keep).cuda()] for t in out], ref, V)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,V", [(200, 9000), (500, 12345), (3, 100000)])
+def test_rows_that_defeat_the_filter(M, V, dtype):
+    """Rising rows and rows of one value, in every launch form: each value
+    passes the bound that was known when it came."""
+    z = torch.linspace(-30, 30, V).repeat(M, 1)
+    z[1::3] = torch.arange(V) * 2.0 ** -10
+    z[2::3] = 1.5
+    z = z.to(dtype)
+    tok = np.arange(M, dtype=np.int32)
+    out, _ = _call(z.cuda(), torch.from_numpy(tok).cuda(), 20, 0.7)
+    rows = [0, 1, 2, M - 1]
+    ref = oracle.token_logprobs(z[rows].double().numpy(), tok[rows], 0.7, 20)
+    _compare([t[rows] for t in out], ref, V)
+
+
+def test_longest_row():
+    V = 1 << 24
+    g = torch.Generator().manual_seed(0)
+    z = torch.randn((1, V), generator=g) * 2
+    out, _ = _call(z.cuda(), torch.tensor([V - 1], dtype=torch.int32).cuda(), 8)
+    z64 = z.double().numpy()
+    lp, lse, ent = oracle.row_logprobs(z64[0])
+    s, e = _tol(V)
+    _close(out[0], lp[-1:], s)
+    _close(out[2], np.array([ent]), e)
+    _close(out[3], np.array([lse]), s)
+    best = np.argpartition(-z64[0], 20)[:20]
+    order = sorted(best, key=lambda v: (-z64[0, v], v))[:8]
+    assert out[5][0].tolist() == order
+    assert int(out[1]) == 1 + int((z64[0] > z64[0, -1]).sum())
+
+
 def test_token_outside_the_vocabulary():
     import block_draft_selection_b200 as bds
     M, V = 4, 700
