@@ -47,6 +47,7 @@ struct Args {
   uint2* q;
   float* scale;
   float eps;
+  float inv_d;
   int d8;
 };
 
@@ -149,18 +150,19 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_kernel(const Args p) {
       red_a[warp] = a;
     }
     __syncthreads();
-    ss = 0.f;
-    a = 0.f;
-    for (int w = 0; w < nwarps; ++w) {
-      if (NORM) ss += red_s[w];
-      if (I8) a = max_nan(a, red_a[w]);
+    const int w = lane & (MAXT / 32 - 1);   // every group of MAXT / 32 lanes adds all warps'
+    ss = w < nwarps ? red_s[w] : 0.f;
+    a = w < nwarps ? red_a[w] : 0.f;
+#pragma unroll
+    for (int off = MAXT / 64; off; off >>= 1) {
+      if (NORM) ss += __shfl_xor_sync(FULL, ss, off);
+      if (I8) a = max_nan(a, __shfl_xor_sync(FULL, a, off));
     }
   }
-  const int d = p.d8 * 8;
   float r = 1.f;
   if (NORM) {
     if (ss < INFINITY) {
-      r = 1.f / sqrtf(ss / static_cast<float>(d) + p.eps);
+      r = rsqrtf(fmaf(ss, p.inv_d, p.eps));   // off by 2 units in the last place at most
     } else {
       // fp32 overflowed (or the row holds a NaN or an infinity): again in fp64
       double s = 0.0;
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_kernel(const Args p) {
       __syncthreads();   // uniform: every thread holds the same ss
       s = 0.0;
       for (int w = 0; w < nwarps; ++w) s += red_d[w];
-      r = static_cast<float>(1.0 / sqrt(s / d + static_cast<double>(p.eps)));
+      r = static_cast<float>(1.0 / sqrt(s / (8 * p.d8) + static_cast<double>(p.eps)));
     }
   }
   if (I8) {
@@ -190,7 +192,8 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_kernel(const Args p) {
     // 127 p must stay in fp32's range: both sides of the quotient times a power of two
     const float k = NORM && a > 1.2676506e30f ? 5.421010862e-20f : 1.f;   // 2^100, 2^-64
     const float num = 127.f * k, den = a * k;
-    const float inv = none ? 0.f : (NORM ? 127.f / a : __fdiv_ru(127.f, a));
+    // the norm's is checked by its remainder, so that 1e-6 would do
+    const float inv = none ? 0.f : (NORM ? num * __fdividef(1.f, den) : __fdiv_ru(127.f, a));
     const F2 inv2(inv, inv), num2(num, num), nden2(-den, -den), magic2(MAGIC, MAGIC), nmagic2(-MAGIC, -MAGIC);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -241,10 +244,10 @@ static cudaError_t launch_as(const Args& a, int M, cudaStream_t st) {
                        dim3(static_cast<unsigned>(threads)), 0, st, a);
 }
 
-// At most one row per SM: one vector per thread ([8, 2560] int8 2.1 us, with two
-// vectors 2.3, with four 2.7; [64, 2560] 2.2, 2.4, 2.9).  More rows: two vectors
-// in the norm ([512, 2560] int8 3.2 us, with one 4.2, with four 4.5;
-// [4352, 4096] int8 23, 37, 30; bf16 23.6, 26.5, 24.0), four in the quantiser,
+// At most one row per SM: one vector per thread ([8, 2560] int8 1.9 us; with two
+// vectors 1.1 times that, with four 1.3).  More rows: two vectors in the norm
+// ([512, 2560] int8 3.1 us, with one 1.3 times that, with four 1.2;
+// [4352, 4096] int8 22, 1.6 and 1.05; bf16 23.7, 1.1, 1.02), four in the quantiser,
 // which holds no sum and no residual ([151936, 2560] 191 us, with one 316, with
 // two 207).
 template <bool NORM, bool I8>
@@ -280,7 +283,7 @@ extern "C" int dflash_rmsnorm(const dflash_bf16* x, const dflash_bf16* residual,
   if (bad_norm(x, residual, gamma, eps, M, d, h) || !y || misaligned(y, 16) || y == h) return DFLASH_ERR_INVALID_ARG;
   Args a = {reinterpret_cast<const uint4*>(x), reinterpret_cast<const uint4*>(residual),
             reinterpret_cast<const uint4*>(gamma), reinterpret_cast<uint4*>(h), reinterpret_cast<uint4*>(y),
-            nullptr, nullptr, eps, d / 8};
+            nullptr, nullptr, eps, 1.f / static_cast<float>(d), d / 8};
   return launch<true, false>(a, M, static_cast<cudaStream_t>(stream));
 }
 
@@ -291,7 +294,7 @@ extern "C" int dflash_rmsnorm_i8(const dflash_bf16* x, const dflash_bf16* residu
     return DFLASH_ERR_INVALID_ARG;
   Args a = {reinterpret_cast<const uint4*>(x), reinterpret_cast<const uint4*>(residual),
             reinterpret_cast<const uint4*>(gamma), reinterpret_cast<uint4*>(h), nullptr,
-            reinterpret_cast<uint2*>(q), scale, eps, d / 8};
+            reinterpret_cast<uint2*>(q), scale, eps, 1.f / static_cast<float>(d), d / 8};
   return launch<true, true>(a, M, static_cast<cudaStream_t>(stream));
 }
 
@@ -300,6 +303,6 @@ extern "C" int dflash_quant_i8(const dflash_bf16* x, int M, int d, int8_t* q, fl
   if (!x || !q || !scale || bad_rows(M, d) || misaligned(x, 16) || misaligned(q, 8) || misaligned(scale, 4))
     return DFLASH_ERR_INVALID_ARG;
   Args a = {reinterpret_cast<const uint4*>(x), nullptr, nullptr, nullptr, nullptr, reinterpret_cast<uint2*>(q),
-            scale, 0.f, d / 8};
+            scale, 0.f, 0.f, d / 8};
   return launch<false, true>(a, M, static_cast<cudaStream_t>(stream));
 }

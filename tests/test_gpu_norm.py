@@ -4,10 +4,11 @@ fp64 oracle.
 h and q must equal the oracle's bit for bit: h is one rounding of a sum that
 fp32 holds well enough for it, and q is decided exactly (see the kernel).
 y: relative 2^-8 for its rounding to bf16 plus the fp32 arithmetic's: a sum of
-squares of at most 32 terms in a row per thread, 5 shuffle levels and 32
-warps (69 roundings, halved by the square root), then a division, an
-addition, a square root, a division and two products -- 41 * 2^-24.  scale:
-the same 41, with a product and a division in place of the two products."""
+squares of at most 32 terms in a row per thread, 5 shuffle levels and up to 32
+warps added one after another (69 roundings, halved by the square root), then
+the mean, the reciprocal square root (two units in the last place: 4 * 2^-24)
+and two products -- 41 * 2^-24.  scale: the same 41, with a product and a
+division in place of the two products."""
 import numpy as np
 import pytest
 import torch
