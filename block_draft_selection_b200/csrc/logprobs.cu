@@ -363,10 +363,11 @@ struct Shared {
   double origin, base, log_s;       // z's log-probability: ((z - origin) c - base) per_t - log_s
 };
 
-// Rank the n entries of `list` by counting and hand each with its rank to put.
-template <int NW, typename F>
+// Rank the n entries of `list` by counting, by all warps but the first, and
+// hand each with its rank to put.
+template <int NT, typename F>
 __device__ __forceinline__ void rank_entries(const uint64_t* list, int n, int K, F put) {
-  for (int i = threadIdx.x; i < n; i += NW * 32) {
+  for (int i = static_cast<int>(threadIdx.x) - 32; i >= 0 && i < n; i += NT - 32) {
     const uint64_t mine = list[i];
     int rank = 0;
 #pragma unroll 8
@@ -600,7 +601,58 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
     }
   }
 
-  // the warp's sums and the last bound
+  // Noted rounds that still count have their values listed; the round's
+  // vectors are read again (from the ring where the whole part is still in it).
+  // Each lane's first one is on its way before the sums and the last bound.
+  uint4 again[U];
+  auto read_again = [&](uint64_t note) {
+    const int r = static_cast<int>(static_cast<uint32_t>(note) / 32), ln = static_cast<int>(note % 32);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int at = u * 32 + ln, v = w_begin + r * STAGE + at;
+      again[u] = make_uint4(fill, fill, fill, fill);
+      if (rounds <= S && v >= in_begin && v < in_end)
+        again[u] = ring[r * CHUNK + at];
+      else if (v < v_end)
+        again[u] = load_vec(z, v * E - lead, p.V);
+    }
+  };
+  auto list_values = [&](uint64_t note) {
+    const int first = (w_begin + static_cast<int>(static_cast<uint32_t>(note) / 32) * STAGE + static_cast<int>(note % 32)) * E - lead;
+    uint64_t bits = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float y[E];
+      Vec<Z>::unpack(again[u], y);
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (!(y[j] < tau) && !(y[j] == -INFINITY)) bits |= 1ull << (u * E + j);
+    }
+    int to = atomicAdd(&sh.n_list, __popcll(bits));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float y[E];
+      Vec<Z>::unpack(again[u], y);
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (bits >> (u * E + j) & 1) {
+          if (to < LIST) sh.list[to] = entry_of(y[j], first + u * 32 * E + j);
+          ++to;
+        }
+    }
+  };
+  auto note_at = [&](int i) -> uint64_t {   // 0 if it does not count any more
+    const uint64_t e = i < min(notes, CAP) ? sh.note[warp * CAP + i] : 0;
+    return static_cast<uint32_t>(e >> 32) >= tau_key ? e : 0;
+  };
+  uint64_t note = 0;
+  if (p.K > 0) {
+    __syncwarp();   // the warp's notes are its lanes'
+    note = note_at(lane);
+    if (note != 0) read_again(note);
+    publish();
+  }
+  // the warp's sums
   {
     float s, w, s1, w1;
     add2(s2[0], s2[1]).get(s, s1);
@@ -619,35 +671,15 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
     cnt = __reduce_add_sync(FULL, cnt);
     if (lane == 0) sh.part[warp] = Sums{big, cnt, s, w};
   }
-  if (p.K > 0) publish();
   __syncthreads();
-  Sums sum;
   if (p.K > 0) {
     bound();
-    // the noted rounds that still count, and their values: the round's vectors
-    // are read again (from the ring where the whole part is still in it)
-    for (int i = lane; i < min(notes, CAP); i += 32) {
-      const uint64_t e = sh.note[warp * CAP + i];
-      if (static_cast<uint32_t>(e >> 32) >= tau_key) {
-        const uint32_t id = static_cast<uint32_t>(e);
-        const int r = id / 32, ln = id % 32;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int at = u * 32 + ln, v = w_begin + r * STAGE + at;
-          uint4 vec = make_uint4(fill, fill, fill, fill);
-          if (rounds <= S && v >= in_begin && v < in_end)
-            vec = ring[r * CHUNK + at];
-          else if (v < v_end)
-            vec = load_vec(z, v * E - lead, p.V);
-          float x[E];
-          Vec<Z>::unpack(vec, x);
-#pragma unroll
-          for (int j = 0; j < E; ++j)
-            if (!(x[j] < tau) && !(x[j] == -INFINITY)) {
-              const int to = atomicAdd(&sh.n_list, 1);
-              if (to < LIST) sh.list[to] = entry_of(x[j], v * E - lead + j);
-            }
-        }
+    if (note != 0 && static_cast<uint32_t>(note >> 32) >= tau_key) list_values(note);
+    for (int i = lane + 32; i < min(notes, CAP); i += 32) {
+      note = note_at(i);
+      if (note != 0) {
+        read_again(note);
+        list_values(note);
       }
     }
     if (__syncthreads_or(notes > CAP) || sh.n_list > LIST) {   // the same for all threads
@@ -657,11 +689,11 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
       for (int v0 = w_begin; v0 < v_begin + rounds * STAGE; v0 += STAGE) {
         for (int u = 0; u < U; ++u) {
           const int v = v0 + u * 32 + lane;
-          float x[E];
-          Vec<Z>::unpack(v < v_end ? load_vec(z, v * E - lead, p.V) : make_uint4(fill, fill, fill, fill), x);
+          float y[E];
+          Vec<Z>::unpack(v < v_end ? load_vec(z, v * E - lead, p.V) : make_uint4(fill, fill, fill, fill), y);
 #pragma unroll
           for (int j = 0; j < E; ++j)
-            top.offer(!(x[j] < tau) && !(x[j] == -INFINITY) ? entry_of(x[j], v * E - lead + j) : 0, p.K, lane);
+            top.offer(!(y[j] < tau) && !(y[j] == -INFINITY) ? entry_of(y[j], v * E - lead + j) : 0, p.K, lane);
         }
       }
       __syncthreads();
@@ -669,13 +701,14 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
       __syncthreads();
     }
   }
-  // the CTA's sums by the first warp
+
+  // From here the first warp has the sums, the others rank the alternatives.
+  int n = p.K > 0 ? sh.n_list : 0;
+  Sums sum;
   if (warp == 0) {
     sum = sh.part[lane & (NW - 1)];
-    sum.reduce<NW>();
+    sum.template reduce<NW>();
   }
-  const int n_list = p.K > 0 ? sh.n_list : 0;
-
   if (Q > 1) {
     // hand list and sums to the cluster's first CTA
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -687,17 +720,16 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
     }
     if (p.K > 0) {
       const uint32_t to = mapa_shared(smem_addr(sh.all + q * MAX_K), 0);
-      rank_entries<NW>(sh.list, n_list, p.K, [&](int rank, uint64_t e) { st_cluster_u64(to + 8 * rank, e); });
-      if (tid >= n_list && tid < p.K) st_cluster_u64(to + 8 * tid, 0);
+      rank_entries<NT>(sh.list, n, p.K, [&](int rank, uint64_t e) { st_cluster_u64(to + 8 * rank, e); });
+      if (tid >= n && tid < p.K) st_cluster_u64(to + 8 * tid, 0);
     }
     cluster_sync_all();
     if (q != 0) return;
     if (warp == 0) {
       const int i = lane & (MAX_Q - 1);
       sum = i < Q ? sh.sums[i] : Sums{-INFINITY, 0, 0.0, 0.0};
-      sum.reduce<MAX_Q>();
-    }
-    if (p.K > 0) {
+      sum.template reduce<MAX_Q>();
+    } else if (p.K > 0) {
       // the largest of the CTAs' K-th entries bounds the row's K-th from below
       uint64_t least = lane < Q ? sh.all[lane * MAX_K + p.K - 1] : 0;
 #pragma unroll
@@ -706,23 +738,19 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
         least = o > least ? o : least;
       }
       least = __shfl_sync(FULL, least, 0);
-      for (int i = tid; i < Q * MAX_K; i += NT) {
+      for (int i = tid - 32; i < Q * MAX_K; i += NT - 32) {
         const uint64_t e = (i & (MAX_K - 1)) < p.K ? sh.all[i] : 0;
         if (e != 0 && e >= least) sh.list[atomicAdd(&sh.n_all, 1)] = e;
       }
+      named_barrier_sync(1, NT - 32);
+      n = sh.n_all;
     }
   }
+  if (warp != 0 && p.K > 0)
+    rank_entries<NT>(sh.list, n, p.K, [&](int rank, uint64_t e) { sh.all[rank] = e; });
 
   // the row's results but for the alternatives, by one lane
-  double origin = 0.0;
-  if (__syncthreads_or(tid == 0 && !(fabsf(sum.base) < FAR) && sum.base != -INFINITY)) {
-    double s, w;
-    origin = far_sums<Z, NT>(z, p.V, p.c, sh, s, w);
-    sum.base = 0.f;
-    sum.s = s;
-    sum.w = w;
-  }
-  if (tid == 0) {
+  auto finish = [&](double origin) {
     const bool dead = sum.base == -INFINITY && sum.s == 0.0;
     const double from = dead ? 0.0 : sum.base;
     const double mean_t = sum.w * recip(sum.s);
@@ -738,16 +766,26 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
       p.logp[row] = bad_token ? __int_as_float(0x7fc00000) : static_cast<float>(v);
     }
     if (p.rank != nullptr) p.rank[row] = bad_token ? 0 : sum.cnt + 1;
+  };
+  const bool far = tid == 0 && !(fabsf(sum.base) < FAR) && sum.base != -INFINITY;
+  if (tid == 0 && !far) finish(0.0);
+  if (__syncthreads_or(far)) {
+    double s, w;
+    const double origin = far_sums<Z, NT>(z, p.V, p.c, sh, s, w);
+    sum.base = 0.f;
+    sum.s = s;
+    sum.w = w;
+    if (tid == 0) finish(origin);
+    __syncthreads();
   }
   if (p.K == 0) return;
-  __syncthreads();
-  const int n = Q > 1 ? sh.n_all : n_list;
+  if (Q > 1) n = sh.n_all;   // the first warp's too
   auto out = [&](int rank, uint64_t e) {
     const size_t o = static_cast<size_t>(row) * p.K + rank;
     p.top_logp[o] = static_cast<float>(((value_of(e) - sh.origin) * p.c - sh.base) * p.per_t - sh.log_s);
     p.top_idx[o] = index_of(e);
   };
-  rank_entries<NW>(sh.list, n, p.K, out);
+  if (tid < min(n, p.K)) out(tid, sh.all[tid]);
   // fewer than K values that are not -inf: the first of -inf, by one warp
   if (n < p.K && warp == NW - 1) {
     int have = n;
@@ -790,6 +828,7 @@ static cudaError_t launch_rows(int rows, Args& a, cudaStream_t st) {
     return launch_rows<Z, 512, 4, 3, 1>(rows, a, st);
   }
   if (2 * rows <= 3 * sms && a.V >= 2 * 4096) a.Q = 2;
+  a.eager = a.Q * rows <= 3 * sms;
   return launch_rows<Z, 256, 4, 3, 3>(rows, a, st);
 }
 
