@@ -629,16 +629,17 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
         if (!(y[j] < tau) && !(y[j] == -INFINITY)) bits |= 1ull << (u * E + j);
     }
     int to = atomicAdd(&sh.n_list, __popcll(bits));
+    for (; bits != 0; bits &= bits - 1, ++to) {   // one or two
+      const int el = __ffsll(static_cast<long long>(bits)) - 1;
+      float v = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float y[E];
-      Vec<Z>::unpack(again[u], y);
+      for (int u = 0; u < U; ++u) {
+        float y[E];
+        Vec<Z>::unpack(again[u], y);
 #pragma unroll
-      for (int j = 0; j < E; ++j)
-        if (bits >> (u * E + j) & 1) {
-          if (to < LIST) sh.list[to] = entry_of(y[j], first + u * 32 * E + j);
-          ++to;
-        }
+        for (int j = 0; j < E; ++j) v = el == u * E + j ? y[j] : v;
+      }
+      if (to < LIST) sh.list[to] = entry_of(v, first + el / E * (32 * E) + el % E);
     }
   };
   auto note_at = [&](int i) -> uint64_t {   // 0 if it does not count any more
