@@ -3,7 +3,7 @@
 //   h = bf16(x + residual),  r = 1 / sqrt(mean h^2 + eps),  y = h gamma r
 //   int8: a = max |h gamma|, scale = a r / 127, q = rint(127 h gamma / a)
 //
-// One CTA per row; the row stays in registers (VPT vectors of 8 channels per
+// One CTA per row (or one warp, for many short ones); the row stays in registers (VPT vectors of 8 channels per
 // thread), so every input byte is read once.  r cancels in q, so the sum of
 // squares and the maximum come out of one block reduction and nothing waits
 // for r before the second pass over the registers.  Memory bound: what counts
@@ -49,6 +49,7 @@ struct Args {
   float eps;
   float inv_d;
   int d8;
+  int M;
 };
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
@@ -80,15 +81,18 @@ __device__ __noinline__ uint2 divide8(uint4 h, uint4 g, float num, float den) {
   return make_uint2(w[0], w[1]);
 }
 
-// MINB: CTAs on an SM that the registers must allow.
-template <int VPT, int MAXT, int MINB, bool NORM, bool I8>
+// MINB: CTAs on an SM that the registers must allow.  ROWS: rows of a CTA,
+// one with all of its warps, or one for each warp (threadIdx.y).
+template <int VPT, int MAXT, int MINB, int ROWS, bool NORM, bool I8>
 __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_kernel(const Args p) {
   __shared__ float red_s[MAXT / 32], red_a[MAXT / 32];
   __shared__ double red_d[MAXT / 32];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = blockDim.x >> 5;
-  const size_t row = static_cast<size_t>(blockIdx.x) * p.d8;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarps = ROWS > 1 ? 1 : blockDim.x >> 5;
+  const unsigned m = ROWS > 1 ? blockIdx.x * ROWS + threadIdx.y : blockIdx.x;
+  if (ROWS > 1 && m >= static_cast<unsigned>(p.M)) return;   // no barrier follows with a row to each warp
+  const size_t row = static_cast<size_t>(m) * p.d8;
   uint4 hv[VPT];
   {
     uint4 rv[VPT];
@@ -177,17 +181,19 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_kernel(const Args p) {
       }
 #pragma unroll
       for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(FULL, s, off);
-      if (lane == 0) red_d[warp] = s;
-      __syncthreads();   // uniform: every thread holds the same ss
-      s = 0.0;
-      for (int w = 0; w < nwarps; ++w) s += red_d[w];
+      if (nwarps > 1) {
+        if (lane == 0) red_d[warp] = s;
+        __syncthreads();   // uniform: every thread holds the same ss
+        s = 0.0;
+        for (int w = 0; w < nwarps; ++w) s += red_d[w];
+      }
       r = static_cast<float>(1.0 / sqrt(s / (8 * p.d8) + static_cast<double>(p.eps)));
     }
   }
   if (I8) {
     const bool bad = !(a < INFINITY);
     const bool zero = a < 7.8886091e-31f;   // 2^-100
-    if (tid == 0) p.scale[blockIdx.x] = bad ? __int_as_float(0x7fc00000) : (zero ? 0.f : a * r / 127.f);
+    if (tid == 0) p.scale[m] = bad ? __int_as_float(0x7fc00000) : (zero ? 0.f : a * r / 127.f);
     const bool none = bad || zero;
     // 127 p must stay in fp32's range: both sides of the quotient times a power of two
     const float k = NORM && a > 1.2676506e30f ? 5.421010862e-20f : 1.f;   // 2^100, 2^-64
@@ -237,30 +243,41 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_kernel(const Args p) {
   }
 }
 
-template <int VPT, int MAXT, int MINB, bool NORM, bool I8>
-static cudaError_t launch_as(const Args& a, int M, cudaStream_t st) {
-  const int threads = ((a.d8 + VPT - 1) / VPT + 31) & ~31;
-  return launch_kernel(rmsnorm_kernel<VPT, MAXT, MINB, NORM, I8>, dim3(static_cast<unsigned>(M)),
-                       dim3(static_cast<unsigned>(threads)), 0, st, a);
+template <int VPT, int MAXT, int MINB, int ROWS, bool NORM, bool I8>
+static cudaError_t launch_as(const Args& a, cudaStream_t st) {
+  const unsigned threads = ROWS > 1 ? 32 : ((a.d8 + VPT - 1) / VPT + 31) & ~31;
+  const unsigned grid = (static_cast<unsigned>(a.M) + ROWS - 1) / ROWS;
+  return launch_kernel(rmsnorm_kernel<VPT, MAXT, MINB, ROWS, NORM, I8>, dim3(grid), dim3(threads, ROWS), 0, st, a);
 }
 
 // At most one row per SM: one vector per thread ([8, 2560] int8 1.9 us; with two
-// vectors 1.1 times that, with four 1.3).  More rows: two vectors in the norm
+// vectors 1.1 times that, with four 1.3).  More rows of up to 512 channels in the
+// norm, 2048 in the quantiser: a warp each, eight in a CTA ([4352, 512] bf16 3.0
+// us, with a CTA each 4.9; [70768, 384] to int8 20, with a CTA each 74, as fast as
+// CTAs start; but [4352, 1024] in the norm 7.0 and 6.4).  Longer rows: two vectors in the norm
 // ([512, 2560] int8 3.1 us, with one 1.3 times that, with four 1.2;
 // [4352, 4096] int8 22, 1.6 and 1.05; bf16 23.7, 1.1, 1.02), four in the quantiser,
 // which holds no sum and no residual ([151936, 2560] 191 us, with one 316, with
 // two 207).
 template <bool NORM, bool I8>
-static int launch(const Args& a, int M, cudaStream_t st) {
+static int launch(const Args& a, cudaStream_t st) {
   cudaError_t e;
   if (a.d8 > 1024)
-    e = launch_as<4, 1024, 1, NORM, I8>(a, M, st);
-  else if (M <= num_sms_current())
-    e = launch_as<1, 1024, 1, NORM, I8>(a, M, st);
+    e = launch_as<4, 1024, 1, 1, NORM, I8>(a, st);
+  else if (a.M <= num_sms_current())
+    e = launch_as<1, 1024, 1, 1, NORM, I8>(a, st);
+  else if (a.d8 <= 32)
+    e = launch_as<1, 256, 5, 8, NORM, I8>(a, st);
+  else if (a.d8 <= 64)
+    e = launch_as<2, 256, 5, 8, NORM, I8>(a, st);
   else if constexpr (NORM)
-    e = launch_as<2, 512, 3, NORM, I8>(a, M, st);
+    e = launch_as<2, 512, 3, 1, NORM, I8>(a, st);
+  else if (a.d8 <= 128)
+    e = launch_as<4, 256, 5, 8, NORM, I8>(a, st);
+  else if (a.d8 <= 256)
+    e = launch_as<8, 256, 4, 8, NORM, I8>(a, st);
   else
-    e = launch_as<4, 256, 5, NORM, I8>(a, M, st);
+    e = launch_as<4, 256, 5, 1, NORM, I8>(a, st);
   return e == cudaSuccess ? DFLASH_OK : DFLASH_ERR_CUDA;
 }
 
@@ -283,8 +300,8 @@ extern "C" int dflash_rmsnorm(const dflash_bf16* x, const dflash_bf16* residual,
   if (bad_norm(x, residual, gamma, eps, M, d, h) || !y || misaligned(y, 16) || y == h) return DFLASH_ERR_INVALID_ARG;
   Args a = {reinterpret_cast<const uint4*>(x), reinterpret_cast<const uint4*>(residual),
             reinterpret_cast<const uint4*>(gamma), reinterpret_cast<uint4*>(h), reinterpret_cast<uint4*>(y),
-            nullptr, nullptr, eps, 1.f / static_cast<float>(d), d / 8};
-  return launch<true, false>(a, M, static_cast<cudaStream_t>(stream));
+            nullptr, nullptr, eps, 1.f / static_cast<float>(d), d / 8, M};
+  return launch<true, false>(a, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int dflash_rmsnorm_i8(const dflash_bf16* x, const dflash_bf16* residual, const dflash_bf16* gamma,
@@ -294,8 +311,8 @@ extern "C" int dflash_rmsnorm_i8(const dflash_bf16* x, const dflash_bf16* residu
     return DFLASH_ERR_INVALID_ARG;
   Args a = {reinterpret_cast<const uint4*>(x), reinterpret_cast<const uint4*>(residual),
             reinterpret_cast<const uint4*>(gamma), reinterpret_cast<uint4*>(h), nullptr,
-            reinterpret_cast<uint2*>(q), scale, eps, 1.f / static_cast<float>(d), d / 8};
-  return launch<true, true>(a, M, static_cast<cudaStream_t>(stream));
+            reinterpret_cast<uint2*>(q), scale, eps, 1.f / static_cast<float>(d), d / 8, M};
+  return launch<true, true>(a, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int dflash_quant_i8(const dflash_bf16* x, int M, int d, int8_t* q, float* scale, void* stream) {
@@ -303,6 +320,6 @@ extern "C" int dflash_quant_i8(const dflash_bf16* x, int M, int d, int8_t* q, fl
   if (!x || !q || !scale || bad_rows(M, d) || misaligned(x, 16) || misaligned(q, 8) || misaligned(scale, 4))
     return DFLASH_ERR_INVALID_ARG;
   Args a = {reinterpret_cast<const uint4*>(x), nullptr, nullptr, nullptr, nullptr, reinterpret_cast<uint2*>(q),
-            scale, 0.f, 0.f, d / 8};
-  return launch<false, true>(a, M, static_cast<cudaStream_t>(stream));
+            scale, 0.f, 0.f, d / 8, M};
+  return launch<false, true>(a, static_cast<cudaStream_t>(stream));
 }

@@ -58,7 +58,9 @@ def _check(x, res, g, eps=1e-6):
 
 @pytest.mark.parametrize("residual", [False, True])
 @pytest.mark.parametrize("M,d", [(1, 8), (1, 256), (3, 264), (8, 2560), (447, 4096), (5, 4104), (64, 5120), (2, 8192),
-                                 (3, 8200), (2, 16384), (1, 32768), (1000, 40)])
+                                 (3, 8200), (2, 16384), (1, 32768), (1000, 40),
+                                 (301, 256), (150, 264), (333, 512), (201, 520), (1001, 1024), (203, 1032),
+                                 (5003, 8)])
 def test_norm(M, d, residual):
     _check(*_inputs(M, d, M + d, residual))
 
@@ -69,18 +71,19 @@ def test_eps(eps):
     _check(x, res, g, eps)
 
 
-def test_extreme_rows():
+@pytest.mark.parametrize("repeat", [1, 60])   # a CTA a row; more rows than SMs: a warp a row where d allows it
+@pytest.mark.parametrize("d", [2560, 640])
+def test_extreme_rows(d, repeat):
     """Rows of zeros, of values whose squares leave fp32, of tiny values, one
     value alone, negative gamma; the squares' sum is taken in fp64 where fp32
     overflows."""
-    d = 2560
     rng = np.random.default_rng(5)
     X = rng.standard_normal((7, d)).astype(np.float32)
     X[0] = 0
     X[1] *= 2.0 ** 80
     X[2] *= 2.0 ** -60
     X[3] = 0
-    X[3, 1234] = -7
+    X[3, 234] = -7
     X[4] = 3e38
     X[5] = 127 * np.where(rng.random(d) < 0.5, 0.5, -1.5) / 2 ** 7
     X[5, 0] = 127
@@ -90,7 +93,7 @@ def test_extreme_rows():
         x = X.copy()
         if gamma[0] not in (1.0, 0.25):
             x[4] = 1e37         # 3e38 times gamma would leave fp32
-        _check(bits(x), None, bits(gamma))
+        _check(bits(np.tile(x, (repeat, 1))), None, bits(gamma))
 
 
 def test_non_finite_rows():
@@ -114,7 +117,8 @@ def test_non_finite_rows():
     assert torch.isnan(y[3, 500].float()) and not y[3, :500].float().any()   # 1 / inf
 
 
-@pytest.mark.parametrize("M,d", [(1, 8), (5, 264), (96, 5120), (777, 2560), (3, 32768)])
+@pytest.mark.parametrize("M,d", [(1, 8), (5, 264), (96, 5120), (777, 2560), (3, 32768), (500, 128), (301, 384),
+                                 (999, 1000)])
 def test_quant(M, d):
     import block_draft_selection_b200 as bds
     rng = np.random.default_rng(M * d)
