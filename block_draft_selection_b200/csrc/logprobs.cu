@@ -21,7 +21,7 @@
 // The row streams through shared memory: each thread copies its own 16-byte
 // vectors (cp.async) S - 1 rounds ahead and reads them back itself, so the
 // loop has no barrier for its data, and the bytes in flight do not cost
-// registers.  (Bulk copies of a warp's whole chunk were measured instead: the
+// registers.  (Bulk copies of a warp's vectors as one chunk were measured instead: the
 // longer way through the copy engine costs more than the load instructions
 // saved, 31 against 19 us for 8 rows of 151936 on one CTA each.)
 //
@@ -51,8 +51,7 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int MAX_K = 32;
 constexpr int MAX_V = 1 << 24;
 constexpr int MAX_Q = 8;            // CTAs that share a row: a cluster
-constexpr int NOTES = 1024;         // rounds a CTA can note
-constexpr int LIST = 512;           // entries ranked at the end: as many as the warps' lists hold
+constexpr int LIST = 512;           // entries ranked at the end: as many as 16 warps' lists hold
 constexpr float LAG = 64.f;
 constexpr float FAR = 1e29f;        // |base| stops here: the row is far
 constexpr float LOW = -1e30f;       // terms below this z c are none
@@ -352,6 +351,7 @@ struct RowToken {
 
 // Shared memory of a CTA beside its ring; `all` and `sums` of the cluster's
 // first CTA take every CTA's list and sums.
+template <int NOTES>
 struct Shared {
   uint64_t note[NOTES];             // (key of the round's maximum, round * 32 + lane), per warp
   uint64_t list[LIST];              // entries to be ranked
@@ -379,8 +379,8 @@ __device__ __forceinline__ void rank_entries(const uint64_t* list, int n, int K,
 // The sums of a row from differences to its maximum, by one CTA: for rows
 // whose values times c leave fp32.  Returns the maximum; s and w in every
 // thread.
-template <typename Z, int NT>
-__device__ __noinline__ float far_sums(const Z* z, int V, float c, Shared& sh, double& s, double& w) {
+template <typename Z, int NT, typename SharedT>
+__device__ __noinline__ float far_sums(const Z* z, int V, float c, SharedT& sh, double& s, double& w) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float m = -INFINITY;
   for (int v = threadIdx.x; v < V; v += NT) m = fmaxf(m, Vec<Z>::load(z + v));
@@ -418,12 +418,14 @@ template <typename Z, int NT, int U, int S, int CTAS>
 __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
   constexpr int E = Vec<Z>::E;
   constexpr int NW = NT / 32;
+  constexpr int NOTES = NT < 256 ? 4 * NT : 1024;   // rounds a CTA can note
   constexpr int CAP = NOTES / NW;     // a warp's notes
   constexpr int STAGE = U * NT;       // vectors per round
-  static_assert(NW * 32 <= LIST && NW <= 16 && MAX_Q * MAX_K <= LIST, "lists fit");
-  constexpr int CHUNK = U * 32;       // vectors per warp and round
+  static_assert(NW * 32 <= LIST && NW > 1 && NW <= 16 && MAX_Q * MAX_K <= LIST, "lists fit");
+  constexpr int CHUNK = U * 32;       // vectors per warp and round: U times 32, NT apart
+  constexpr int SPAN = STAGE - NT + 32;   // from their first to past their last
   extern __shared__ uint4 ring_all[];   // [NW][S][CHUNK]
-  __shared__ Shared sh;
+  __shared__ Shared<NOTES> sh;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -445,18 +447,18 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
   // vectors [in_begin, in_end) lie inside the row whole
   const int in_begin = lead > 0 ? 1 : 0, in_end = min(v_end, (p.V + lead) / E);
   const uint4* zv = reinterpret_cast<const uint4*>(z - lead);
-  const int w_begin = v_begin + warp * CHUNK;   // this warp's chunk of round 0
+  const int w_begin = v_begin + warp * 32;   // this warp's first vector of round 0
   // This lane's copies of round r: its vectors that lie inside the row whole.
   auto fetch = [&](int r) {
     const int v0 = w_begin + r * STAGE;
     const uint32_t to = ring_addr + 16 * ((r % S) * CHUNK);
-    if (v0 >= in_begin && v0 + CHUNK <= in_end) {
+    if (v0 >= in_begin && v0 + SPAN <= in_end) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) copy16(to + 16 * u * 32, zv + v0 + u * 32 + lane);
+      for (int u = 0; u < U; ++u) copy16(to + 16 * u * 32, zv + v0 + u * NT + lane);
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int v = v0 + u * 32 + lane;
+        const int v = v0 + u * NT + lane;
         if (v >= in_begin && v < in_end) copy16(to + 16 * u * 32, zv + v);
       }
     }
@@ -467,10 +469,10 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
   auto take = [&](int r) {
     const int v0 = w_begin + r * STAGE;
     const uint4* at = ring + (r % S) * CHUNK + lane;
-    const bool whole = v0 >= in_begin && v0 + CHUNK <= in_end;
+    const bool whole = v0 >= in_begin && v0 + SPAN <= in_end;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int v = v0 + u * 32 + lane;
+      const int v = v0 + u * NT + lane;
       uint4 vec;
       if (whole || (v >= in_begin && v < in_end))
         vec = at[u * 32];
@@ -609,7 +611,7 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
     const int r = static_cast<int>(static_cast<uint32_t>(note) / 32), ln = static_cast<int>(note % 32);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int at = u * 32 + ln, v = w_begin + r * STAGE + at;
+      const int at = u * 32 + ln, v = w_begin + r * STAGE + u * NT + ln;
       again[u] = make_uint4(fill, fill, fill, fill);
       if (rounds <= S && v >= in_begin && v < in_end)
         again[u] = ring[r * CHUNK + at];
@@ -639,7 +641,7 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
 #pragma unroll
         for (int j = 0; j < E; ++j) v = el == u * E + j ? y[j] : v;
       }
-      if (to < LIST) sh.list[to] = entry_of(v, first + el / E * (32 * E) + el % E);
+      if (to < LIST) sh.list[to] = entry_of(v, first + el / E * (NT * E) + el % E);
     }
   };
   auto note_at = [&](int i) -> uint64_t {   // 0 if it does not count any more
@@ -647,11 +649,12 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
     return static_cast<uint32_t>(e >> 32) >= tau_key ? e : 0;
   };
   uint64_t note = 0;
+  const bool fresh = next_bound == 4 * rounds - 1;   // the last round ended with a bound
   if (p.K > 0) {
     __syncwarp();   // the warp's notes are its lanes'
     note = note_at(lane);
     if (note != 0) read_again(note);
-    publish();
+    if (!fresh) publish();
   }
   // the warp's sums
   {
@@ -674,7 +677,7 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
   }
   __syncthreads();
   if (p.K > 0) {
-    bound();
+    if (!fresh) bound();
     if (note != 0 && static_cast<uint32_t>(note >> 32) >= tau_key) list_values(note);
     for (int i = lane + 32; i < min(notes, CAP); i += 32) {
       note = note_at(i);
@@ -689,7 +692,7 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
       WarpTop top{0, 0};
       for (int v0 = w_begin; v0 < v_begin + rounds * STAGE; v0 += STAGE) {
         for (int u = 0; u < U; ++u) {
-          const int v = v0 + u * 32 + lane;
+          const int v = v0 + u * NT + lane;
           float y[E];
           Vec<Z>::unpack(v < v_end ? load_vec(z, v * E - lead, p.V) : make_uint4(fill, fill, fill, fill), y);
 #pragma unroll
@@ -819,11 +822,30 @@ static cudaError_t launch_rows(int rows, const Args& a, cudaStream_t st) {
 // 32 rows 12.7 / 14.6, 64 rows 17.0 / 18.6, 148 rows 24.3 / 29.4; 200 rows 32.5
 // with two CTAs, 37.6 with one, 43.5 in the first form; 300 rows 47.8 with one,
 // 51.4 with two.  Clusters of 16 measured 16 us for 8 rows.
+//
+// What a row costs beside its values (barriers, bound, ranking) falls with the
+// CTA's size, so short rows and many rows go to smaller CTAs, more of them on an
+// SM.  us, against the forms above, fp32 with K = 16 (bf16 with K = 20 where it
+// says so): 128 threads, 100 rows of 2000 4.8 / 5.7 and of 4000 5.8 / 5.7; 200
+// of 8000 7.5 / 7.0; 600 of 8000 11.6 / 13.5 and of 16000 17.5 / 18.7, 500 of
+// 64000 bf16 33.2 / 29.2; 1700 of 129280 169 / 173, 4352 of 64000 bf16 152 / 174,
+// 4352 of 8000 52 / 73.  64 threads: 4352 of 1000 18.5 / 54.5 (128: 29.4), of
+// 4000 34.4 / 56.9 (40.1), of 8000 52.3 / 73.2 (51.0); 600 of 1000 5.8 / 10.6
+// (7.1), of 4000 9.3 / 10.5 (9.0); 100 of 1000 5.2 / 5.6 (4.7).
 template <typename Z>
 static cudaError_t launch_rows(int rows, Args& a, cudaStream_t st) {
   const int sms = num_sms_current();
-  a.eager = rows <= sms;
+  const long long n_vec = (static_cast<long long>(a.V) * sizeof(Z) + 15) / 16;
   a.Q = 1;
+  if (n_vec <= (rows > 8 * sms ? 1024 : 256) && rows > 2 * sms) {
+    a.eager = rows <= 12 * sms;
+    return launch_rows<Z, 64, 4, 2, 12>(rows, a, st);
+  }
+  if (n_vec <= 512 || (n_vec <= 4096 && rows > 2 * sms) || rows > 6 * sms) {
+    a.eager = rows <= 6 * sms;
+    return launch_rows<Z, 128, 4, 3, 6>(rows, a, st);
+  }
+  a.eager = rows <= sms;
   if (a.eager) {
     while (a.Q < MAX_Q && 2 * a.Q * rows <= sms && a.V / (2 * a.Q) >= 4096) a.Q *= 2;
     return launch_rows<Z, 512, 4, 3, 1>(rows, a, st);

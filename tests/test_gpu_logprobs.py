@@ -100,11 +100,14 @@ def test_alternatives_and_temperatures(K, T):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("V", [40, 5000, 140000])
-def test_masks_and_orders(V, dtype):
+@pytest.mark.parametrize("V,copies", [(40, 1), (5000, 1), (140000, 1), (40, 90), (1000, 1), (1000, 20), (1500, 90),
+                                      (4000, 30), (4000, 90), (9000, 80), (20000, 60)])
+def test_masks_and_orders(V, copies, dtype):
     """Rows a mask leaves nothing, one or two tokens of; the lowest and the
     largest value of the type; constant rows; ties; rising and falling rows;
-    +0 and -0; a row with one certain token."""
+    +0 and -0; a row with one certain token; the same many times over, in the
+    forms for many rows.  (Threads of the smallest form sum V / 256 terms, not
+    V / 512: the tolerance of a row twice as long.)"""
     lowest = torch.finfo(dtype).min
     rng = np.random.default_rng(V)
     M = 16
@@ -132,10 +135,10 @@ def test_masks_and_orders(V, dtype):
     z[15] = -60.0
     tok = np.full(M, V // 2, np.int32)
     K = 32
-    out, status = _call(z.cuda(), torch.from_numpy(tok).cuda(), K)
-    assert status == 0
     ref = oracle.token_logprobs(z.double().numpy(), tok, 1.0, K)
-    _compare(out, ref, V)
+    out, status = _call(z.cuda().repeat(copies, 1), torch.from_numpy(tok).cuda().repeat(copies), K)
+    assert status == 0
+    _compare(out, {k: np.concatenate([v] * copies) for k, v in ref.items()}, 2 * V if copies > 1 else V)
     assert out[0][0] == -math.inf and out[3][0] == -math.inf and out[2][0] == 0
 
 
@@ -160,8 +163,9 @@ def test_nan_and_infinity(dtype):
     assert ti[1, 1:].tolist() == [v for v in order if v != 2500][:3]
 
 
-def test_rows_not_asked_for_keep_what_they_held():
-    M, V, K = 9, 5000, 16
+@pytest.mark.parametrize("M,V", [(9, 5000), (9, 500), (300, 900), (1900, 300)])
+def test_rows_not_asked_for_keep_what_they_held(M, V):
+    K = 16
     z, z64 = _logits(M, V, 1)
     tok, _ = _tokens(M, V, 1)
     tok[[0, 4, 8]] = [-1, -100, -1]
@@ -197,7 +201,8 @@ def test_padding_among_rows_that_clusters_share():
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("M,V", [(200, 9000), (500, 12345), (3, 100000)])
+@pytest.mark.parametrize("M,V", [(200, 9000), (500, 12345), (3, 100000), (20, 2000), (330, 1000), (1300, 3000),
+                                 (1000, 40000)])
 def test_rows_that_defeat_the_filter(M, V, dtype):
     """Rising rows and rows of one value, in every launch form: each value
     passes the bound that was known when it came."""
@@ -257,7 +262,7 @@ def test_without_tokens():
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("B,L,V,pad", [(1, 1, 64, 0), (1, 7, 151936, 0), (16, 5, 5000, 3), (40, 16, 3000, 0),
-                                       (3, 32, 4097, 0)])
+                                       (3, 32, 4097, 0), (90, 16, 700, 1)])
 def test_emitted(B, L, V, pad, dtype):
     import block_draft_selection_b200 as bds
     z, z64 = _logits(B * (L + 1), V, B + L, dtype, pad)
@@ -308,9 +313,10 @@ def test_rows_past_32_bit_offsets():
     _compare([t[rows] for t in out], ref, V)
 
 
-def test_repeatable():
-    z, _ = _logits(5, 151936, 11, torch.bfloat16)
-    _, tok = _tokens(5, 151936, 11)
+@pytest.mark.parametrize("M,V", [(5, 151936), (400, 800), (400, 8000)])
+def test_repeatable(M, V):
+    z, _ = _logits(M, V, 11, torch.bfloat16)
+    _, tok = _tokens(M, V, 11)
     first, _ = _call(z, tok, 32, 0.7)
     for _ in range(5):
         for a, b in zip(first, _call(z, tok, 32, 0.7)[0]):
