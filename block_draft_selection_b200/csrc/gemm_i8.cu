@@ -22,8 +22,14 @@
 //          not started yet and takes its tile (cluster launch control).
 //          The accumulator's rows are tokens; the epilogue turns blocks of
 //          32 x 32 through shared memory and stores whole rows of them, from
-//          any alignment of C.
-//   LARGE  (M > 128): channels on the M side, tokens on the N side, in steps of
+//          any alignment of C.  With N <= 128 < M the operands change places:
+//          few channels on the M side, the tokens as the long operand
+//          ([4352 x 5 x 5120] took 70 us on LARGE's tiles, mostly empty).
+//   SPLIT  the same with few tiles: a cluster of up to 8 CTAs to a tile, each
+//          with a part of K.  Each leaves its int32 sums in its shared memory
+//          and adds up its share of the tile over the cluster's: integers, so
+//          the result is the same.  No more clusters than run at once.
+//   LARGE  (else): channels on the M side, tokens on the N side, in steps of
 //          32 instead of 128 (448 tokens are two tiles of 224).  Tiles of 256
 //          channels x up to 256 tokens on a cluster of two CTAs that share one
 //          tcgen05.mma.cta_group::2 (each CTA stages half of either operand and
@@ -57,18 +63,22 @@ constexpr int EPI_THREADS = 32 * EPI_WARPS;
 constexpr int NUM_THREADS = 64 + EPI_THREADS;
 constexpr int SMEM_BUDGET = 226 * 1024;
 constexpr int MAX_STAGES = 24;
+constexpr int MAX_SPLIT = 8;            // SPLIT: a portable cluster
 constexpr int MAX_K = 131071;           // 128 * 128 * K stays below 2^31
 constexpr int MAX_ROWS = 0x7fffff00;    // tile arithmetic stays in int
 
-enum { STREAM, LARGE, LARGE_PAIR };
+enum { STREAM, SPLIT, LARGE, LARGE_PAIR };
 
 struct Params {
-  int M, N;
+  int M, N;           // STREAM, SPLIT with `swapped`: of the exchanged operands
+  int swapped;        // what is called tokens here are rows of B, the channels rows of A
+  int split;          // SPLIT: CTAs that share a tile's K
   int num_kc;         // K stages per tile
   int stages;
   int tt;             // tokens per tile (MMA N)
   int t_rows;         // token rows this CTA loads (half of tt in a pair)
   int t_stage_bytes;  // stage bytes of the tokens
+  int pitch;          // SPLIT: of the sums in shared memory, elements a row of C
   int tmem_cols;      // two accumulators of half as many columns each
   int height;         // channels of a tile that this CTA loads (LARGE: 128)
   int c_stage_bytes;  // stage bytes of the channels
@@ -186,10 +196,20 @@ __device__ __forceinline__ void load32(uint32_t taddr, int (&v)[32]) {
 __device__ __forceinline__ void put(float* c, float v) { *c = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* c, float v) { *c = __float2bfloat16_rn(v); }
 
+__device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 template <int MODE, typename OUT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_i8_kernel(const __grid_constant__ CUtensorMap tm_t, const __grid_constant__ CUtensorMap tm_c, const Params p) {
   constexpr bool PAIR = MODE == LARGE_PAIR;
+  constexpr bool FEW = MODE == STREAM || MODE == SPLIT;   // one tile of tokens, on the M side
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -214,8 +234,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
-  const bool leader = rank == 0;
+  const uint32_t rank = PAIR || MODE == SPLIT ? cluster_ctarank() : 0u;
+  const bool leader = !PAIR || rank == 0;
   const uint32_t peer_abort = PAIR ? mapa_shared(smem_addr(const_cast<int*>(abort_flag)), rank ^ 1u) : 0u;
 
   if (threadIdx.x == 0) {
@@ -254,13 +274,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int tmem_stride = p.tmem_cols >> 1;
-  const int first_tile = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
+  const int first_tile = PAIR            ? static_cast<int>(blockIdx.x >> 1)
+                         : MODE == SPLIT ? static_cast<int>(blockIdx.x) / p.split
+                                         : static_cast<int>(blockIdx.x);
+  // this CTA's part of K
+  const int k_begin = MODE == SPLIT ? static_cast<int>(rank) * p.num_kc / p.split : 0;
+  const int k_end = MODE == SPLIT ? (static_cast<int>(rank) + 1) * p.num_kc / p.split : p.num_kc;
   if (warp == 0 && lane == 0) {
     // B is a weight: its first stages may come into L2 while the kernel before
     // this one ends (L2 is the point of coherence, so nothing stale is seen
     // should that kernel write it after all)
     const Tile t = tile_at<PAIR>(p, first_tile, rank);
-    for (int kc = 0; kc < p.w_prefetch && kc < p.num_kc; ++kc) tma_prefetch_l2_2d(&tm_c, kc * BK, t.c0);
+    for (int kc = k_begin; kc < k_begin + p.w_prefetch && kc < k_end; ++kc) tma_prefetch_l2_2d(&tm_c, kc * BK, t.c0);
   }
   pdl_wait();
 
@@ -292,6 +317,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // The tile after `i`, the it-th of this CTA, in all lanes of a warp; -1 at
   // the end, or when a wait gives up.
   auto next_tile = [&](int i, int it, bool counted) {
+    if (MODE == SPLIT) return -1;
     if (MODE != STREAM) {
       const int step = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
       return i < p.tiles - step ? i + step : -1;
@@ -305,7 +331,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   int issued = 0;   // producer: stage loads issued, in ring order
   int asked = 0;    // producer: tiles asked for
   if (warp == 0) {
-    const uint64_t pol_c = MODE == STREAM ? l2_policy_evict_first() : l2_policy_evict_normal();
+    const uint64_t pol_c = FEW ? l2_policy_evict_first() : l2_policy_evict_normal();
     const uint64_t pol_t = l2_policy_evict_last();
     int s = 0;
     uint32_t ph = 0;
@@ -327,8 +353,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ++asked;
       }
       const Tile t = tile_at<PAIR>(p, i, rank);
-      const int t0 = t.m0 + static_cast<int>(rank) * p.t_rows;
-      for (int kc = 0; kc < p.num_kc; ++kc) {
+      const int t0 = t.m0 + (PAIR ? static_cast<int>(rank) * p.t_rows : 0);
+      for (int kc = k_begin; kc < k_end; ++kc) {
         if (!ready && !wait(empty_bar(s), ph ^ 1u)) {
           ok = false;
           break;
@@ -354,7 +380,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   } else if (warp == 1) {
     if (leader) {
-      const uint32_t idesc = umma_idesc_s8(PAIR ? 2 * CH : CH, MODE == STREAM ? p.height : p.tt);
+      const uint32_t idesc = umma_idesc_s8(PAIR ? 2 * CH : CH, FEW ? p.height : p.tt);
       int s = 0, tb = 0;
       uint32_t ph = 0, tph = 0;
       bool ok = true, ready = false;
@@ -368,7 +394,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!wait(tempty_bar(tb), tph ^ 1u)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(tb * tmem_stride);
-        for (int kc = 0; kc < p.num_kc; ++kc) {
+        for (int kc = k_begin; kc < k_end; ++kc) {
           if (!ready && !wait(full_bar(s), ph)) {
             ok = false;
             break;
@@ -379,12 +405,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tc_fence_after();
           const uint64_t cdesc = umma_desc_sw128(s_c + s * p.c_stage_bytes);
           const uint64_t tdesc = umma_desc_sw128(s_t + s * p.t_stage_bytes);
-          const uint64_t mdesc = MODE == STREAM ? tdesc : cdesc, ndesc = MODE == STREAM ? cdesc : tdesc;
+          const uint64_t mdesc = FEW ? tdesc : cdesc, ndesc = FEW ? cdesc : tdesc;
           const uint32_t eb = empty_bar(s);
           if (elected) {
 #pragma unroll
             for (int kk = 0; kk < BK / UMMA_K; ++kk)   // 32 bytes of K on: the address field counts 16
-              umma_s8<PAIR>(d_tmem, mdesc + 2ull * kk, ndesc + 2ull * kk, idesc, (kc | kk) != 0 ? 1u : 0u);
+              umma_s8<PAIR>(d_tmem, mdesc + 2ull * kk, ndesc + 2ull * kk, idesc, ((kc - k_begin) | kk) != 0 ? 1u : 0u);
             commit(eb);
           }
           ready = __all_sync(0xffffffffu, peek) != 0;
@@ -423,7 +449,44 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc_fence_after();
       const uint32_t taddr =
           tmem_base + static_cast<uint32_t>(tb * tmem_stride) + (static_cast<uint32_t>(quarter * 32) << 16);
-      if constexpr (MODE == STREAM) {
+      if constexpr (MODE == SPLIT) {
+        // the sums over this CTA's part of K into the ring, which every load
+        // and MMA is done with
+        int* part = reinterpret_cast<int*>(smem);
+        const int r = quarter * 32 + lane;
+        for (int b = half; quarter * 32 < p.M && b * 32 < p.height; b += 2) {
+          int x[32];
+          load32(taddr + b * 32, x);
+          if (r < p.M) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              if (b * 32 + j >= p.height) break;   // a multiple of 16
+              if (p.swapped) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) part[(b * 32 + j + k) * p.pitch + r] = x[j + k];
+              } else {
+                *reinterpret_cast<int4*>(part + r * p.pitch + b * 32 + j) = make_int4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+              }
+            }
+          }
+        }
+      } else if (MODE == STREAM && p.swapped) {
+        // lanes are columns of C, registers its rows
+        const int n = quarter * 32 + lane;
+        for (int b = half; quarter * 32 < p.M && b * 32 < p.height && t.c0 + b * 32 < p.N; b += 2) {
+          const int m = t.c0 + b * 32, rows = min(min(32, p.height - b * 32), p.N - m);
+          const float scale = lane < rows ? __ldg(p.sb + m + lane) : 0.f;
+          int x[32];
+          load32(taddr + b * 32, x);
+          OUT* c = static_cast<OUT*>(p.C) + static_cast<size_t>(m) * p.M + n;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float v = __int2float_rn(x[j]) * __shfl_sync(0xffffffffu, scale, j) * sa_row;
+            if (j < rows && n < p.M) put(c, v);
+            c += p.M;
+          }
+        }
+      } else if constexpr (MODE == STREAM) {
         // blocks of 32 tokens (this warp's lanes) x 32 channels; the two warps
         // of a quarter take every other block
         const int m0 = quarter * 32, rows = min(32, p.M - m0);
@@ -481,6 +544,45 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   __syncwarp();
+  if (MODE == SPLIT) {
+    // every CTA adds up its share of the tile's elements over the cluster
+    cluster_sync_all();
+    const Tile t = tile_at<false>(p, first_tile, 0);
+    const int across = min(p.height, p.N - t.c0);
+    const int rows = p.swapped ? across : p.M, cols = p.swapped ? p.M : across;   // of C
+    const float* sa = p.swapped ? p.sb + t.c0 : p.sa;
+    const float* sb = p.swapped ? p.sa : p.sb + t.c0;
+    const size_t ld = p.swapped ? p.M : p.N;
+    OUT* c = static_cast<OUT*>(p.C) + (p.swapped ? t.c0 * ld : static_cast<size_t>(t.c0));
+    const int fours = (cols + 3) / 4, total = rows * fours;   // four elements a thread
+    const int end = static_cast<int>((rank + 1) * total / p.split);
+    uint32_t from[MAX_SPLIT];
+#pragma unroll
+    for (int q = 0; q < MAX_SPLIT; ++q) from[q] = mapa_shared(s_t, q < p.split ? q : 0);
+    for (int e = static_cast<int>(rank * total / p.split) + static_cast<int>(threadIdx.x); e < end; e += NUM_THREADS) {
+      const int m = e / fours, n = 4 * (e - m * fours);
+      const float sam = __ldg(sa + m);
+      float sbn[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) sbn[k] = n + k < cols ? __ldg(sb + n + k) : 0.f;
+      const uint32_t off = 4u * (m * p.pitch + n);
+      int x[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int q = 0; q < MAX_SPLIT; ++q) {
+        if (q >= p.split) break;
+        const int4 v = ld_cluster_v4(from[q] + off);
+        x[0] += v.x;
+        x[1] += v.y;
+        x[2] += v.z;
+        x[3] += v.w;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (n + k < cols) put(c + m * ld + n + k, __int2float_rn(x[k]) * sam * sbn[k]);
+    }
+    __syncwarp();
+    cluster_sync_all();   // nobody's part is read any more
+  }
   if (PAIR) cluster_sync_all();   // every role of both CTAs is done: abort flags and counts are final
   if (warp == 0 && elected && leader && *abort_flag != 0) {
     // Loads issued but never consumed must land before the CTA (and the other
@@ -545,35 +647,37 @@ static cudaError_t allow_smem() {
   return cudaFuncSetAttribute(gemm_i8_kernel<MODE, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BUDGET);
 }
 
-// Clusters of two that can be resident at once on the current device (0:
-// pairs cannot run), asked once per device.
-static int max_pairs() {
+// Clusters of 2, 4 or 8 CTAs with all of the shared memory that can be resident
+// at once on the current device (0: they cannot run), asked once per device.
+template <int MODE>
+static int max_clusters(int size) {
   constexpr int MAX_DEVICES = 64;
-  static std::atomic<int> known[MAX_DEVICES];   // the count plus one; 0: not asked yet
+  static std::atomic<int> known[MAX_DEVICES][4];   // the count plus one; 0: not asked yet
+  const int which = size == 2 ? 1 : size == 4 ? 2 : 3;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   if (dev < MAX_DEVICES) {
-    const int k = known[dev].load(std::memory_order_relaxed);
+    const int k = known[dev][which].load(std::memory_order_relaxed);
     if (k > 0) return k - 1;
   }
-  if (allow_smem<LARGE_PAIR, float>() != cudaSuccess) return 0;
+  if (allow_smem<MODE, float>() != cudaSuccess) return 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2);
+  cfg.gridDim = dim3(size);
   cfg.blockDim = dim3(NUM_THREADS);
   cfg.dynamicSmemBytes = SMEM_BUDGET;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = size;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int c = 0;
-  if (cudaOccupancyMaxActiveClusters(&c, gemm_i8_kernel<LARGE_PAIR, float>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&c, gemm_i8_kernel<MODE, float>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
-  if (dev < MAX_DEVICES) known[dev].store(c + 1, std::memory_order_relaxed);
+  if (dev < MAX_DEVICES) known[dev][which].store(c + 1, std::memory_order_relaxed);
   return c;
 }
 
@@ -600,11 +704,13 @@ static bool make_plan(int M, int N, int K, int sms, Plan& pl) {
   p.M = M;
   p.N = N;
   p.num_kc = (K + BK - 1) / BK;
-  if (M <= CH) {
+  if (M <= CH || N <= CH) {
     pl.mode = STREAM;
-    p.tt = (M + 15) & ~15;
+    p.swapped = M > CH;
+    if (p.swapped) std::swap(p.M, p.N);
+    p.tt = (p.M + 15) & ~15;
     p.t_rows = p.tt;
-    const int units = (N + 15) / 16;
+    const int units = (p.N + 15) / 16;
     // the highest tiles of which every SM gets the same number: fewer tiles
     // are fewer MMAs, and less is read of the tokens for each ([8 x 151936 x
     // 2560]: 13 units high 66 us, 16 units, four for each SM and two left over,
@@ -613,9 +719,38 @@ static bool make_plan(int M, int N, int K, int sms, Plan& pl) {
     const int h = (units + rounds * sms - 1) / (rounds * sms);
     p.height = 16 * h;
     p.m_tiles = 1;
-    p.tiles = pl.grid = (units + h - 1) / h;
+    // Few tiles: K over clusters of 2, 4 or 8 CTAs, higher tiles for it.  A
+    // fit of what was measured, in clocks: a stage 380, or 170 and 4.8 a channel
+    // and 1.1 a token if that is more; an element of the tile 0.32 on its way to
+    // C; 1400 for the cluster's barriers and the other CTAs' sums.  us with 1, 2, 4
+    // and 8 CTAs to a tile, the fit's choice starred: [8 x 64 x 5120] 11.2, 7.0,
+    // 5.3, 4.6*; [8 x 2560 x 2560] 7.3, 6.2, 6.1*, 6.5; [128 x 2560 x 2560] 8.0,
+    // 7.3, 7.4*, 10.0; [128 x 5120 x 5120] 12.9, 10.6*, 11.4; [8 x 5120 x 640] 4.3*,
+    // 5.1, 5.8; [8 x 10000 x 5120] 13.9, 12.4*; [4352 x 5 x 5120] 12.1, 9.3, 9.1*.
+    p.split = 1;
+    long long best = -1;
+    for (int split = 1; split <= MAX_SPLIT && split <= p.num_kc; split *= 2) {
+      const int at_once = split == 1 ? sms : max_clusters<SPLIT>(split);
+      if (at_once < 1) continue;
+      const int hs = split == 1 ? h : (units + at_once - 1) / at_once;
+      if (hs * 16 > MAX_N) break;
+      const long long stage = std::max(3800, 1700 + 48 * 16 * hs + 11 * p.tt);   // tenths of a clock
+      const long long cost = ((p.num_kc + split - 1) / split * stage + 51LL * p.tt * hs) * (split == 1 ? rounds : 1) +
+                             (split > 1 ? 14000 : 0);
+      if (best < 0 || cost < best) {
+        best = cost;
+        p.split = split;
+        p.height = 16 * hs;
+      }
+    }
+    if (p.split > 1) {
+      pl.mode = SPLIT;
+      p.pitch = p.swapped ? (p.M + 3) & ~3 : p.height + 4;
+    }
+    p.tiles = (p.N + p.height - 1) / p.height;
+    pl.grid = p.tiles * p.split;
   } else {
-    const int pairs = pair_allowed() ? max_pairs() : 0;
+    const int pairs = pair_allowed() ? max_clusters<LARGE_PAIR>(2) : 0;
     const bool pair = pairs >= 1;
     pl.mode = pair ? LARGE_PAIR : LARGE;
     const int units = pair ? (pairs < sms / 2 ? pairs : sms / 2) : sms;
@@ -646,7 +781,7 @@ static bool make_plan(int M, int N, int K, int sms, Plan& pl) {
   p.t_stage_bytes = p.t_rows * BK;
   p.c_stage_bytes = p.height * BK;
   p.tmem_cols = 32;
-  const int columns = ((pl.mode == STREAM ? p.height : p.tt) + 31) & ~31;   // read in blocks of 32
+  const int columns = ((pl.mode == STREAM || pl.mode == SPLIT ? p.height : p.tt) + 31) & ~31;   // read in blocks of 32
   while (p.tmem_cols < 2 * columns) p.tmem_cols *= 2;
   for (p.stages = MAX_STAGES; p.stages > 2 && smem_bytes(pl) > SMEM_BUDGET;) --p.stages;
   return smem_bytes(pl) <= SMEM_BUDGET;
@@ -657,7 +792,7 @@ static cudaError_t launch_as(const Plan& pl, const CUtensorMap& tt, const CUtens
   const cudaError_t e = allow_smem<MODE, OUT>();
   if (e != cudaSuccess) return e;
   return launch_kernel_cluster(gemm_i8_kernel<MODE, OUT>, dim3(pl.grid), dim3(NUM_THREADS), smem_bytes(pl), st,
-                               MODE == LARGE_PAIR ? 2 : 1, tt, tc, pl.p);
+                               MODE == LARGE_PAIR ? 2 : MODE == SPLIT ? pl.p.split : 1, tt, tc, pl.p);
 }
 
 }  // namespace gi8
@@ -677,19 +812,22 @@ extern "C" int dflash_gemm_i8(const int8_t* A, const float* sa, const int8_t* B,
   Plan pl;
   if (!make_plan(M, N, K, sms, pl)) return DFLASH_ERR_UNSUPPORTED;
   Params& p = pl.p;
-  p.w_prefetch = pl.mode == STREAM ? 8 : 0;
-  p.sa = sa;
-  p.sb = sb;
+  p.w_prefetch = (pl.mode == STREAM || pl.mode == SPLIT) && !p.swapped ? 8 : 0;
+  p.sa = p.swapped ? sb : sa;
+  p.sb = p.swapped ? sa : sb;
   p.C = C;
   p.status = dev_status;
   p.timeout_ns = timeout_ns_from_env();
   CUtensorMap tt, tc;
-  const bool ok = gi8::make_map(&tt, A, M, K, p.t_rows) && gi8::make_map(&tc, B, N, K, p.height);
+  const bool ok = gi8::make_map(&tt, p.swapped ? B : A, p.swapped ? N : M, K, p.t_rows) &&
+                  gi8::make_map(&tc, p.swapped ? A : B, p.swapped ? M : N, K, p.height);
   if (!ok) return DFLASH_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (pl.mode == STREAM)
     e = c_bf16 ? launch_as<STREAM, __nv_bfloat16>(pl, tt, tc, st) : launch_as<STREAM, float>(pl, tt, tc, st);
+  else if (pl.mode == SPLIT)
+    e = c_bf16 ? launch_as<SPLIT, __nv_bfloat16>(pl, tt, tc, st) : launch_as<SPLIT, float>(pl, tt, tc, st);
   else if (pl.mode == LARGE_PAIR)
     e = c_bf16 ? launch_as<LARGE_PAIR, __nv_bfloat16>(pl, tt, tc, st) : launch_as<LARGE_PAIR, float>(pl, tt, tc, st);
   else

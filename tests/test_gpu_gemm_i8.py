@@ -39,7 +39,13 @@ def _run(A, sa, B, sb, dtype=torch.float32, **kw):
 SHAPES = [(1, 1, 16), (1, 17, 64), (8, 4096, 256), (7, 2560, 2560), (15, 1000, 144), (16, 129, 128), (17, 128, 112),
           (33, 4099, 272), (64, 300, 1040), (127, 257, 128), (128, 640, 400), (129, 255, 256), (130, 2049, 272),
           (160, 33, 96), (192, 16, 512), (255, 513, 128), (256, 256, 256), (257, 1000, 384), (300, 4099, 160),
-          (448, 1030, 640), (512, 31, 2576), (1000, 777, 208), (2049, 129, 64), (3, 40000, 80), (100, 19000, 64)]
+          (448, 1030, 640), (512, 31, 2576), (1000, 777, 208), (2049, 129, 64), (3, 40000, 80), (100, 19000, 64),
+          # few tiles, K over a cluster: two, four and eight CTAs to a tile, parts of unequal length
+          (1, 64, 5120), (8, 70, 1040), (128, 16, 5120), (100, 2560, 2560), (16, 1000, 272), (128, 1027, 1936),
+          (5, 2000, 400), (65, 4500, 1168),
+          # few channels: rows of A as the long operand, alone and over a cluster
+          (300, 1, 5120), (129, 100, 96), (200, 70, 2576), (1000, 5, 1552), (4352, 5, 1040), (2000, 128, 272),
+          (5000, 17, 640), (40000, 3, 80), (50001, 128, 16)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -77,12 +83,12 @@ def test_full_range_values(M, N, K):
     np.testing.assert_array_equal(_run(A, sa, B, sb).cpu().numpy(), oracle.gemm_i8(A, sa, B, sb))
 
 
-@pytest.mark.parametrize("M", [6, 260])
-def test_scales_as_they_are(M):
+@pytest.mark.parametrize("M,N", [(6, 300), (260, 300), (300, 60), (30000, 60)])
+def test_scales_as_they_are(M, N):
     """Zero, negative, infinite and NaN scales reach exactly their rows and columns."""
-    A, sa, B, sb = _inputs(M, 300, 128, 2)
+    A, sa, B, sb = _inputs(M, N, 128, 2)
     sa[:5] = [0.0, -1.5, np.inf, np.nan, 1e-30]
-    sb[7], sb[299] = np.nan, -2.0
+    sb[7], sb[N - 1] = np.nan, -2.0
     with np.errstate(invalid="ignore"):
         ref = oracle.gemm_i8(A, sa, B, sb)
     got = _run(A, sa, B, sb).cpu().numpy()
@@ -91,7 +97,7 @@ def test_scales_as_they_are(M):
     assert np.isnan(got[3]).all() and np.isnan(got[:, 7]).all()
 
 
-@pytest.mark.parametrize("M,N", [(8, 1003), (200, 1003), (200, 1004)])
+@pytest.mark.parametrize("M,N", [(8, 1003), (200, 1003), (200, 1004), (1003, 101), (40001, 7)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_output_at_any_element(M, N, dtype):
     """C inside a larger buffer, aligned to its element only; nothing around it changes."""
@@ -110,7 +116,7 @@ def test_repeatable():
         assert torch.equal(_run(A, sa, B, sb), first)
 
 
-@pytest.mark.parametrize("M,N", [(17000, 129280), (100, 21600000)])
+@pytest.mark.parametrize("M,N", [(17000, 129280), (100, 21600000), (21600000, 100)])
 def test_output_past_32_bit_offsets(M, N):
     """More than 2^31 elements of C: the last rows and columns are checked."""
     import block_draft_selection_b200 as bds

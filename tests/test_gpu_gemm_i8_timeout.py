@@ -1,11 +1,12 @@
 """The int8 product's bounded waits, made to run out on purpose (no fault:
 every wait gives up at its deadline, records DFLASH_ERR_TIMEOUT, drains what it
-has in flight and returns), on its three paths: weight streaming, 2-CTA pairs,
-and single CTAs at the same sizes.  A child process sets DFLASH_TIMEOUT_NS,
-read at every call, far below the call's time, then clears it: the next call
-of the same process must be right.  The budget is each wait's own.  The first
-is far below the time of a tile, for which the epilogue waits, so its call must
-time out; the second is near it, so its call may also complete."""
+has in flight and returns), on its four paths: weight streaming, 2-CTA pairs,
+single CTAs at the same sizes, and K split over clusters.  A child process
+sets DFLASH_TIMEOUT_NS, read at every call, far below the call's time, then
+clears it: the next call of the same process must be right.  The budget is each
+wait's own.  The first is far below the time of a tile, for which the epilogue
+waits, so its call must time out; the second is near it, so its call may also
+complete."""
 import json
 import os
 import subprocess
@@ -21,7 +22,8 @@ pytestmark = pytest.mark.gpu
 # a long K: the epilogue waits about 100 us for a tile's accumulator
 CASES = [(8, 20000, 32768, {}, (2_000, 60_000)),
          (448, 20000, 32768, {}, (2_000, 60_000)),
-         (448, 20000, 32768, {"DFLASH_PAIR": "0"}, (2_000, 60_000))]
+         (448, 20000, 32768, {"DFLASH_PAIR": "0"}, (2_000, 60_000)),
+         (8, 1000, 131056, {}, (2_000, 30_000))]
 
 
 def child(case):
@@ -55,7 +57,7 @@ def child(case):
     print(json.dumps({"codes": codes, "right": right, "timeout_code": bds.DFLASH_ERR_TIMEOUT}), flush=True)
 
 
-@pytest.mark.parametrize("case", range(len(CASES)), ids=["stream", "pairs", "single-ctas"])
+@pytest.mark.parametrize("case", range(len(CASES)), ids=["stream", "pairs", "single-ctas", "split"])
 def test_wait_budget_runs_out_and_context_survives(case):
     out = subprocess.run([sys.executable, os.path.abspath(__file__), "--child", str(case)], cwd=ROOT,
                          capture_output=True, text=True, timeout=600)
