@@ -29,6 +29,8 @@
 //          with a part of K.  Each leaves its int32 sums in its shared memory
 //          and adds up its share of the tile over the cluster's: integers, so
 //          the result is the same.  No more clusters than run at once.
+//          Both also take a few hundred tokens in tiles of up to 128 where
+//          there would be few tiles of pairs with a long K (plan_few).
 //   LARGE  (else): channels on the M side, tokens on the N side, in steps of
 //          32 instead of 128 (448 tokens are two tiles of 224).  Tiles of 256
 //          channels x up to 256 tokens on a cluster of two CTAs that share one
@@ -82,7 +84,7 @@ struct Params {
   int tmem_cols;      // two accumulators of half as many columns each
   int height;         // channels of a tile that this CTA loads (LARGE: 128)
   int c_stage_bytes;  // stage bytes of the channels
-  int m_tiles;        // LARGE
+  int m_tiles;        // tiles of tokens, which run fastest
   int tiles;
   int w_prefetch;     // K stages of B prefetched into L2 before the dependency wait
   const float* sa;
@@ -440,7 +442,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int half = (warp - 2) >> 2;         // which half of the tile's tokens
     const int nch = p.tt / 16, split = (nch + 1) >> 1;
     float* block = reinterpret_cast<float*>(tail + 8 * (2 * p.stages + 10) + 16) + (quarter * 2 + half) * BLOCK;
-    const float sa_row = MODE == STREAM && quarter * 32 + lane < p.M ? __ldg(p.sa + quarter * 32 + lane) : 0.f;
     int tb = 0;
     uint32_t tph = 0;
     for (int i = first_tile, it = 0; i >= 0; ++it) {
@@ -449,15 +450,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc_fence_after();
       const uint32_t taddr =
           tmem_base + static_cast<uint32_t>(tb * tmem_stride) + (static_cast<uint32_t>(quarter * 32) << 16);
+      // FEW: this warp's tokens of the tile, a lane each
+      const int m0 = t.m0 + quarter * 32, rows = min(min(32, p.tt - quarter * 32), p.M - m0);
+      const float sa_row = MODE == STREAM && lane < rows ? __ldg(p.sa + m0 + lane) : 0.f;
       if constexpr (MODE == SPLIT) {
         // the sums over this CTA's part of K into the ring, which every load
         // and MMA is done with
         int* part = reinterpret_cast<int*>(smem);
         const int r = quarter * 32 + lane;
-        for (int b = half; quarter * 32 < p.M && b * 32 < p.height; b += 2) {
+        for (int b = half; rows > 0 && b * 32 < p.height; b += 2) {
           int x[32];
           load32(taddr + b * 32, x);
-          if (r < p.M) {
+          if (lane < rows) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
               if (b * 32 + j >= p.height) break;   // a multiple of 16
@@ -472,24 +476,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       } else if (MODE == STREAM && p.swapped) {
         // lanes are columns of C, registers its rows
-        const int n = quarter * 32 + lane;
-        for (int b = half; quarter * 32 < p.M && b * 32 < p.height && t.c0 + b * 32 < p.N; b += 2) {
-          const int m = t.c0 + b * 32, rows = min(min(32, p.height - b * 32), p.N - m);
-          const float scale = lane < rows ? __ldg(p.sb + m + lane) : 0.f;
+        for (int b = half; rows > 0 && b * 32 < p.height && t.c0 + b * 32 < p.N; b += 2) {
+          const int m = t.c0 + b * 32, tokens = min(min(32, p.height - b * 32), p.N - m);
+          const float scale = lane < tokens ? __ldg(p.sb + m + lane) : 0.f;
           int x[32];
           load32(taddr + b * 32, x);
-          OUT* c = static_cast<OUT*>(p.C) + static_cast<size_t>(m) * p.M + n;
+          OUT* c = static_cast<OUT*>(p.C) + static_cast<size_t>(m) * p.M + m0 + lane;
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const float v = __int2float_rn(x[j]) * __shfl_sync(0xffffffffu, scale, j) * sa_row;
-            if (j < rows && n < p.M) put(c, v);
+            if (j < tokens && lane < rows) put(c, v);
             c += p.M;
           }
         }
       } else if constexpr (MODE == STREAM) {
         // blocks of 32 tokens (this warp's lanes) x 32 channels; the two warps
         // of a quarter take every other block
-        const int m0 = quarter * 32, rows = min(32, p.M - m0);
         for (int b = half; rows > 0 && b * 32 < p.height && t.c0 + b * 32 < p.N; b += 2) {
           int x[32];
           load32(taddr + b * 32, x);
@@ -548,12 +550,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // every CTA adds up its share of the tile's elements over the cluster
     cluster_sync_all();
     const Tile t = tile_at<false>(p, first_tile, 0);
-    const int across = min(p.height, p.N - t.c0);
-    const int rows = p.swapped ? across : p.M, cols = p.swapped ? p.M : across;   // of C
-    const float* sa = p.swapped ? p.sb + t.c0 : p.sa;
-    const float* sb = p.swapped ? p.sa : p.sb + t.c0;
+    const int across = min(p.height, p.N - t.c0), down = min(p.tt, p.M - t.m0);
+    const int rows = p.swapped ? across : down, cols = p.swapped ? down : across;   // of C
+    const int m0 = p.swapped ? t.c0 : t.m0, n0 = p.swapped ? t.m0 : t.c0;
+    const float* sa = (p.swapped ? p.sb : p.sa) + m0;
+    const float* sb = (p.swapped ? p.sa : p.sb) + n0;
     const size_t ld = p.swapped ? p.M : p.N;
-    OUT* c = static_cast<OUT*>(p.C) + (p.swapped ? t.c0 * ld : static_cast<size_t>(t.c0));
+    OUT* c = static_cast<OUT*>(p.C) + m0 * ld + n0;
     const int fours = (cols + 3) / 4, total = rows * fours;   // four elements a thread
     const int end = static_cast<int>((rank + 1) * total / p.split);
     uint32_t from[MAX_SPLIT];
@@ -694,8 +697,56 @@ static size_t smem_bytes(const Plan& pl) {
   const Params& p = pl.p;
   const size_t ring = static_cast<size_t>(p.stages) * (p.c_stage_bytes + p.t_stage_bytes);
   const size_t span = static_cast<size_t>(p.stages - 1) * p.t_stage_bytes + CH * BK;
-  const size_t blocks = pl.mode == STREAM ? sizeof(float) * BLOCK * 2 * ((p.M + 31) / 32) : 0;
+  const size_t blocks = pl.mode == STREAM ? sizeof(float) * BLOCK * 2 * ((p.tt + 31) / 32) : 0;
   return 1024 + std::max(ring + 8 * (2 * p.stages + 10) + 16 + blocks, span);
+}
+
+// Tiles of up to 128 tokens x up to 256 channels: STREAM or SPLIT.  Returns
+// the estimated time in tenths of a clock, -1 if such a tile would not do.
+//
+// Few tiles: K over clusters of 2, 4 or 8 CTAs, higher tiles for it.  The
+// estimate is a fit of what was measured, in clocks: a stage 380, or 2.2 a row
+// of either operand, or 170 and 4.2 a channel where no other CTA reads the same
+// channels; an element of the tile 0.32 on its way to C; the cluster's barriers
+// and the other CTAs' sums 1400; more than one tile of tokens 1000 to 1400.  us
+// with 1, 2, 4 and 8 CTAs to a tile, the choice starred: [8 x 64 x 5120] 11.2,
+// 7.0, 5.3, 4.6*; [8 x 2560 x 2560] 7.3, 6.2, 6.1*, 6.5; [128 x 2560 x 2560] 8.0,
+// 7.3*, 7.4, 10.0; [128 x 5120 x 5120] 12.9, 10.6*, 11.4; [8 x 5120 x 640] 4.3*,
+// 5.1, 5.8; [8 x 10000 x 5120] 13.9, 12.4*; [4352 x 5 x 5120] 12.1, 9.3*, 9.1.
+static long long plan_few(int sms, Plan& pl) {
+  Params& p = pl.p;
+  p.m_tiles = (p.M + CH - 1) / CH;
+  p.tt = ((p.M + p.m_tiles - 1) / p.m_tiles + 15) & ~15;
+  p.t_rows = p.tt;
+  const int units = (p.N + 15) / 16;
+  long long best = -1;
+  for (int split = 1; split <= MAX_SPLIT && split <= p.num_kc; split *= 2) {
+    const int at_once = (split == 1 ? sms : max_clusters<SPLIT>(split)) / p.m_tiles;
+    if (at_once < 1) continue;
+    // the highest tiles of which every SM gets the same number: fewer tiles
+    // are fewer MMAs, and less is read of the tokens for each ([8 x 151936 x
+    // 2560]: 13 units high 66 us, 16 units, four for each SM and two left over,
+    // 70; 8 units 77)
+    const int most = MAX_N / 16 * at_once;
+    const int rounds = split == 1 && p.m_tiles == 1 ? (units + most - 1) / most : 1;
+    const int h = (units + rounds * at_once - 1) / (rounds * at_once);
+    if (h * 16 > MAX_N) continue;
+    const long long stage =
+        std::max({3800, 22 * (16 * h + p.tt), p.m_tiles == 1 ? 1700 + 42 * 16 * h : 0});
+    const long long cost = rounds * ((p.num_kc + split - 1) / split * stage + 51LL * p.tt * h) +
+                           (p.m_tiles == 1 ? (split > 1 ? 14000 : 0) : (split > 1 ? 28000 : 10000));
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.split = split;
+      p.height = 16 * h;
+    }
+  }
+  if (best < 0) return -1;
+  pl.mode = p.split > 1 ? SPLIT : STREAM;
+  p.pitch = p.swapped ? (p.tt + 3) & ~3 : p.height + 4;
+  p.tiles = (p.N + p.height - 1) / p.height * p.m_tiles;
+  pl.grid = p.tiles * p.split;
+  return best;
 }
 
 static bool make_plan(int M, int N, int K, int sms, Plan& pl) {
@@ -705,54 +756,12 @@ static bool make_plan(int M, int N, int K, int sms, Plan& pl) {
   p.N = N;
   p.num_kc = (K + BK - 1) / BK;
   if (M <= CH || N <= CH) {
-    pl.mode = STREAM;
     p.swapped = M > CH;
     if (p.swapped) std::swap(p.M, p.N);
-    p.tt = (p.M + 15) & ~15;
-    p.t_rows = p.tt;
-    const int units = (p.N + 15) / 16;
-    // the highest tiles of which every SM gets the same number: fewer tiles
-    // are fewer MMAs, and less is read of the tokens for each ([8 x 151936 x
-    // 2560]: 13 units high 66 us, 16 units, four for each SM and two left over,
-    // 70; 8 units 77)
-    const int rounds = (units + MAX_N / 16 * sms - 1) / (MAX_N / 16 * sms);
-    const int h = (units + rounds * sms - 1) / (rounds * sms);
-    p.height = 16 * h;
-    p.m_tiles = 1;
-    // Few tiles: K over clusters of 2, 4 or 8 CTAs, higher tiles for it.  A
-    // fit of what was measured, in clocks: a stage 380, or 170 and 4.8 a channel
-    // and 1.1 a token if that is more; an element of the tile 0.32 on its way to
-    // C; 1400 for the cluster's barriers and the other CTAs' sums.  us with 1, 2, 4
-    // and 8 CTAs to a tile, the fit's choice starred: [8 x 64 x 5120] 11.2, 7.0,
-    // 5.3, 4.6*; [8 x 2560 x 2560] 7.3, 6.2, 6.1*, 6.5; [128 x 2560 x 2560] 8.0,
-    // 7.3, 7.4*, 10.0; [128 x 5120 x 5120] 12.9, 10.6*, 11.4; [8 x 5120 x 640] 4.3*,
-    // 5.1, 5.8; [8 x 10000 x 5120] 13.9, 12.4*; [4352 x 5 x 5120] 12.1, 9.3, 9.1*.
-    p.split = 1;
-    long long best = -1;
-    for (int split = 1; split <= MAX_SPLIT && split <= p.num_kc; split *= 2) {
-      const int at_once = split == 1 ? sms : max_clusters<SPLIT>(split);
-      if (at_once < 1) continue;
-      const int hs = split == 1 ? h : (units + at_once - 1) / at_once;
-      if (hs * 16 > MAX_N) break;
-      const long long stage = std::max(3800, 1700 + 48 * 16 * hs + 11 * p.tt);   // tenths of a clock
-      const long long cost = ((p.num_kc + split - 1) / split * stage + 51LL * p.tt * hs) * (split == 1 ? rounds : 1) +
-                             (split > 1 ? 14000 : 0);
-      if (best < 0 || cost < best) {
-        best = cost;
-        p.split = split;
-        p.height = 16 * hs;
-      }
-    }
-    if (p.split > 1) {
-      pl.mode = SPLIT;
-      p.pitch = p.swapped ? (p.M + 3) & ~3 : p.height + 4;
-    }
-    p.tiles = (p.N + p.height - 1) / p.height;
-    pl.grid = p.tiles * p.split;
+    if (plan_few(sms, pl) < 0) return false;
   } else {
     const int pairs = pair_allowed() ? max_clusters<LARGE_PAIR>(2) : 0;
     const bool pair = pairs >= 1;
-    pl.mode = pair ? LARGE_PAIR : LARGE;
     const int units = pair ? (pairs < sms / 2 ? pairs : sms / 2) : sms;
     const int ch = pair ? 2 * CH : CH;
     const long long c_tiles = (static_cast<long long>(N) + ch - 1) / ch;
@@ -761,22 +770,40 @@ static bool make_plan(int M, int N, int K, int sms, Plan& pl) {
     // tokens; [448 x 151936 x 2560]: 6.8, 8.3, 9.5 and 11.6 us a tile of 64,
     // 128, 192 and 256)
     long long best = -1;
-    for (int tt = MAX_N; tt >= 32; tt -= 32) {
-      const long long tiles = c_tiles * ((M + tt - 1) / tt);
-      const long long cost = (tiles + units - 1) / units * (ch + tt);
+    int tt = 0;
+    for (int t = MAX_N; t >= 32; t -= 32) {
+      const long long tiles = c_tiles * ((M + t - 1) / t);
+      const long long cost = (tiles + units - 1) / units * (ch + t);
       if (best < 0 || cost < best) {
         best = cost;
-        p.tt = tt;
+        tt = t;
       }
     }
-    p.m_tiles = (M + p.tt - 1) / p.tt;
-    const long long tiles = c_tiles * p.m_tiles;
+    const long long m_tiles = (M + tt - 1) / tt, tiles = c_tiles * m_tiles;
     if (tiles > 0x7fffffffLL) return false;
-    p.tiles = static_cast<int>(tiles);
-    p.t_rows = pair ? p.tt / 2 : p.tt;
-    p.height = CH;
-    const int used = tiles < units ? static_cast<int>(tiles) : units;
-    pl.grid = pair ? 2 * used : used;
+    // Few tiles of pairs, a long K: the other tiles with K split, if they are
+    // estimated to take less.  A stage of a pair 380 clocks, or 3.3 a token,
+    // a token's accumulators 27 on their way to C, 500 for the pair's barriers.
+    // us, pairs / the others: [130 x 300 x 5120] 10.6 / 6.7*, [192 x 1024 x 5120]
+    // 10.7 / 8.1*, [600 x 600 x 5120] 11.7 / 9.7*, [2000 x 300 x 5120] 13.3 / 10.5*,
+    // [200 x 5120 x 2560] 8.5* / 10.1, [448 x 5120 x 5120] 15.8* / 18.4.
+    const long long cost = (tiles + units - 1) / units * p.num_kc * std::max(3800, 33 * tt) + 270LL * tt + 5000;
+    bool few = false;
+    if (pair && M <= CH * sms) {
+      const long long other = plan_few(sms, pl);
+      few = other >= 0 && other < cost;
+    }
+    if (!few) {
+      pl.mode = pair ? LARGE_PAIR : LARGE;
+      p.split = 1;
+      p.tt = tt;
+      p.m_tiles = static_cast<int>(m_tiles);
+      p.tiles = static_cast<int>(tiles);
+      p.t_rows = pair ? tt / 2 : tt;
+      p.height = CH;
+      const int used = tiles < units ? static_cast<int>(tiles) : units;
+      pl.grid = pair ? 2 * used : used;
+    }
   }
   p.t_stage_bytes = p.t_rows * BK;
   p.c_stage_bytes = p.height * BK;

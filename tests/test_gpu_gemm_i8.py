@@ -43,6 +43,9 @@ SHAPES = [(1, 1, 16), (1, 17, 64), (8, 4096, 256), (7, 2560, 2560), (15, 1000, 1
           # few tiles, K over a cluster: two, four and eight CTAs to a tile, parts of unequal length
           (1, 64, 5120), (8, 70, 1040), (128, 16, 5120), (100, 2560, 2560), (16, 1000, 272), (128, 1027, 1936),
           (5, 2000, 400), (65, 4500, 1168),
+          # more than 128 tokens in few tiles, and so many that pairs take them
+          (130, 300, 2576), (192, 1024, 5120), (600, 600, 1040), (1000, 300, 2064), (145, 1003, 4112), (130, 38500, 80),
+          (333, 20001, 144), (1500, 5003, 272), (2500, 2051, 400),
           # few channels: rows of A as the long operand, alone and over a cluster
           (300, 1, 5120), (129, 100, 96), (200, 70, 2576), (1000, 5, 1552), (4352, 5, 1040), (2000, 128, 272),
           (5000, 17, 640), (40000, 3, 80), (50001, 128, 16)]
