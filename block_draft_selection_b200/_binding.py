@@ -9,6 +9,7 @@ computation runs in the library's kernels; there is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -650,6 +651,17 @@ def _logprob_outs(shape, K, index, stream, logp, rank, entropy, lse, top_logp, t
     if not 0 <= K <= 32:
         raise ValueError(f"K must be in [0, 32], got {K}")
     f32, i32 = torch.float32, torch.int32
+    if with_token and logp is rank is entropy is lse is top_logp is top_idx is None:
+        # none given: parts of one buffer, zeroed by one launch instead of six
+        n = math.prod(shape)
+        flat = _new(f32, (n * (4 + 2 * K),), index, stream, torch.zeros)
+        logp, rank, entropy, lse, top_logp, top_idx = flat.split((n, n, n, n, n * K, n * K))
+        outs = (logp, rank.view(i32), entropy, lse, top_logp.view(*shape, K), top_idx.view(i32).view(*shape, K))
+        if len(shape) > 1:
+            outs = (*(t.view(shape) for t in outs[:4]), *outs[4:])
+        p = flat.data_ptr()
+        ptrs = tuple(p + 4 * n * i for i in (0, 1, 2, 3, 4, 4 + K))
+        return outs, ptrs if K else (*ptrs[:4], None, None)
     if with_token:
         logp, p0 = _logprob_out(logp, "logp", f32, shape, index, stream)
         rank, p1 = _logprob_out(rank, "rank", i32, shape, index, stream)

@@ -343,3 +343,29 @@ def test_arguments_refused():
                       (lambda: bds.dflash_token_logprobs(z[:0], t[:0]), bds.DFlashError)):
         with pytest.raises(err):
             call()
+
+
+@pytest.mark.parametrize("K", [0, 3])
+def test_outputs_not_given(K):
+    """Outputs the call allocates: their shapes and types, each contiguous and apart from the others, zero
+    where no row asked; the same on a stream of the caller's."""
+    import block_draft_selection_b200 as bds
+    z, z64 = _logits(6, 77, 12)
+    tok = np.array([3, -1, 0, 76, -1, 40], np.int32)
+    dtok = torch.from_numpy(tok).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    keep = torch.from_numpy(tok >= 0).cuda()
+    ref = oracle.token_logprobs(z64[tok >= 0], tok[tok >= 0], 1.0, K)
+    for stream in (None, side):
+        out = bds.dflash_token_logprobs(z, dtok, K=K, stream=stream)
+        torch.cuda.synchronize()
+        types = [torch.float32, torch.int32, torch.float32, torch.float32, torch.float32, torch.int32]
+        assert [t.dtype for t in out] == types and all(t.is_contiguous() for t in out)
+        assert [tuple(t.shape) for t in out] == [(6,)] * 4 + [(6, K)] * 2
+        assert all(not t[~keep].any() for t in out)
+        _compare([t[keep] for t in out], ref, 77)
+        kept = [t.clone() for t in out]
+        for i, t in enumerate(out):
+            t.fill_(9)
+            assert all(torch.equal(out[j], kept[j]) for j in range(i + 1, 6))
