@@ -3,11 +3,11 @@
 //   h = bf16(x + residual),  r = 1 / sqrt(mean h^2 + eps),  y = h gamma r
 //   int8: a = max |h gamma|, scale = a r / 127, q = rint(127 h gamma / a)
 //
-// One CTA per row (or one warp, for many short ones); the row stays in registers (VPT vectors of 8 channels per
-// thread), so every input byte is read once.  r cancels in q, so the sum of
-// squares and the maximum come out of one block reduction and nothing waits
-// for r before the second pass over the registers.  Memory bound: what counts
-// is bytes in flight.  Many rows take few threads with up to 8 vectors each,
+// One CTA per row, or one warp where there are many short ones; the row stays
+// in registers (VPT vectors of 8 channels per thread), so every input byte is
+// read once.  r cancels in q, so the sum of squares and the maximum come out of
+// one reduction and nothing waits for r before the second pass over the
+// registers.  Memory bound: what counts is bytes in flight.  Many rows take few threads with up to 8 vectors each,
 // all loaded before the first is used, and as many CTAs as fit on an SM; few
 // rows take one vector per thread, where the shortest chain counts.
 //
@@ -254,11 +254,11 @@ static cudaError_t launch_as(const Args& a, cudaStream_t st) {
 // vectors 1.1 times that, with four 1.3).  More rows of up to 512 channels in the
 // norm, 2048 in the quantiser: a warp each, eight in a CTA ([4352, 512] bf16 3.0
 // us, with a CTA each 4.9; [70768, 384] to int8 20, with a CTA each 74, as fast as
-// CTAs start; but [4352, 1024] in the norm 7.0 and 6.4).  Longer rows: two vectors in the norm
-// ([512, 2560] int8 3.1 us, with one 1.3 times that, with four 1.2;
-// [4352, 4096] int8 22, 1.6 and 1.05; bf16 23.7, 1.1, 1.02), four in the quantiser,
-// which holds no sum and no residual ([151936, 2560] 191 us, with one 316, with
-// two 207).
+// CTAs start; but [4352, 1024] in the norm 7.0 and 6.4).  Longer rows: two
+// vectors in the norm ([512, 2560] int8 3.1 us, with one 1.3 times that, with
+// four 1.2; [4352, 4096] int8 22, 1.6 and 1.05; bf16 23.7, 1.1, 1.02), four in the
+// quantiser, which holds no sum and no residual ([151936, 2560] 191 us, with one
+// 316, with two 207).
 template <bool NORM, bool I8>
 static int launch(const Args& a, cudaStream_t st) {
   cudaError_t e;
