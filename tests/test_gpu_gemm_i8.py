@@ -151,3 +151,30 @@ def test_shapes_and_types_refused():
         bds.dflash_gemm_i8(A[:, :24].contiguous(), sa, B[:, :24].contiguous(), sb)     # K % 16
     with pytest.raises(bds.DFlashError):
         bds.dflash_gemm_i8(A[:0], sa[:0], B, sb)
+
+
+def test_calls_at_once_and_replayed():
+    """Products of every form on three streams at once, and captured and replayed with new inputs."""
+    import block_draft_selection_b200 as bds
+    cases = [_inputs(M, N, K, M + N) for M, N, K in ((8, 64, 5120), (600, 600, 1040), (4352, 5, 1040), (96, 20000, 256),
+                                                     (448, 5000, 640))]
+    refs = [torch.from_numpy(oracle.gemm_i8(*c)) for c in cases]
+    dev = [_dev(*c) for c in cases]
+    outs = [[torch.empty(c[0].shape[0], c[2].shape[0], device="cuda") for c in cases] for _ in range(3)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, stream in enumerate(streams):
+            for i in range(len(cases)):
+                bds.dflash_gemm_i8(*dev[(i + s) % len(cases)], C=outs[s][(i + s) % len(cases)], stream=stream)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(c.cpu(), r) for c, r in zip(o, refs))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = [bds.dflash_gemm_i8(*d) for d in dev]
+    for d in dev:
+        d[0].neg_()                                            # values in [-127, 127]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(c.cpu(), -r) for c, r in zip(captured, refs))
