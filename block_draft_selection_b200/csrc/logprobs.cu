@@ -7,12 +7,15 @@
 // rows still fill the GPU).  Each thread keeps a reference `base` (the largest
 // z c it has seen, or nearly), s = sum exp2(t) and w = sum t exp2(t) with
 // t = z c - base, c = log2(e) / T, one fused multiply-add, and the count of
-// values above z_t.  base is a value in fp32, not z c rounded: the results are
-// relative to it, so its rounding cancels.  It moves only when a value exceeds
-// it by more than LAG: terms up to 2^LAG cost no precision, and rescaling is
-// rare.  Where |base| would pass 1e29 (a row that holds nothing above a mask of
-// the type's lowest value, or an infinity) the row's sums are taken again from
-// differences z - max; values below -1e30 / c count as that value.
+// values above z_t.  base is a value in fp32 to which the results are relative,
+// so it cancels; but it is z c rounded, and the largest term is 2 to the power
+// of what the rounding took away, up to half a unit of base's last place.  So
+// |base| stops at FAR = 2^28, up to which that is 8.  Below -FAR a thread's terms are
+// as good as none beside any row's that has a value above it (a finite mask),
+// and a row that holds nothing within +-FAR (masked as a whole, or of a very
+// low temperature, or with an infinity) has its sums taken again from
+// differences z - max.  base moves only when a value exceeds it by more than
+// LAG, so that rescaling is rare.  Values below -1e30 / c count as that value.
 //
 // c is rounded to fp32, i.e. the sums are those of a temperature off by a
 // relative 2^-24; the log of the sum is corrected for that to first order with
@@ -53,7 +56,7 @@ constexpr int MAX_V = 1 << 24;
 constexpr int MAX_Q = 8;            // CTAs that share a row: a cluster
 constexpr int LIST = 512;           // entries ranked at the end: as many as 16 warps' lists hold
 constexpr float LAG = 64.f;
-constexpr float FAR = 1e29f;        // |base| stops here: the row is far
+constexpr float FAR = 268435456.f;  // 2^28: |base| stops here, the row is far
 constexpr float LOW = -1e30f;       // terms below this z c are none
 constexpr uint32_t LOWEST_KEY = 0x00800000u;   // of the lowest finite value
 constexpr double LN2 = 0.69314718055994530942;
@@ -377,24 +380,40 @@ __device__ __forceinline__ void rank_entries(const uint64_t* list, int n, int K,
 }
 
 // The sums of a row from differences to its maximum, by one CTA: for rows
-// whose values times c leave fp32.  Returns the maximum; s and w in every
-// thread.
+// whose largest value times c is beyond FAR.  Returns the maximum; s and w in
+// every thread.
 template <typename Z, int NT, typename SharedT>
 __device__ __noinline__ float far_sums(const Z* z, int V, float c, SharedT& sh, double& s, double& w) {
+  constexpr int E = Vec<Z>::E;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(Z)), n_vec = (V + lead + E - 1) / E;
   float m = -INFINITY;
-  for (int v = threadIdx.x; v < V; v += NT) m = fmaxf(m, Vec<Z>::load(z + v));
+#pragma unroll 4
+  for (int v = threadIdx.x; v < n_vec; v += NT) {
+    float y[E];
+    Vec<Z>::unpack(load_vec(z, v * E - lead, V), y);
+#pragma unroll
+    for (int j = 0; j < E; ++j) m = fmaxf(m, y[j]);
+  }
   m = warp_max(m);
   __syncthreads();
   if (lane == 0) sh.part[warp].base = m;
   __syncthreads();
   for (int k = 0; k < NT / 32; ++k) m = fmaxf(m, sh.part[k].base);
   s = w = 0.0;
-  for (int v = threadIdx.x; v < V; v += NT) {
-    const float t = max_nan((Vec<Z>::load(z + v) - m) * c, -200.f);
-    const float e = ex2(t);
-    s += e;
-    w += static_cast<double>(e) * t;
+#pragma unroll 4
+  for (int v = threadIdx.x; v < n_vec; v += NT) {
+    float y[E], se = 0.f, we = 0.f;
+    Vec<Z>::unpack(load_vec(z, v * E - lead, V), y);
+#pragma unroll
+    for (int j = 0; j < E; ++j) {   // outside the row -inf: a term of 0
+      const float t = max_nan((y[j] - m) * c, -200.f);
+      const float e = ex2(t);
+      se += e;
+      we = fmaf(e, t, we);
+    }
+    s += se;   // a vector's terms in fp32, vectors in fp64
+    w += we;
   }
   for (int off = 16; off; off >>= 1) {
     s += __shfl_xor_sync(FULL, s, off);
