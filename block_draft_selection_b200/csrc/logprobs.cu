@@ -4,18 +4,25 @@
 //   entropy = -sum p log p,  the K largest z (value desc, index asc)
 //
 // One pass over a row, which a cluster of Q CTAs shares (Q chosen so that few
-// rows still fill the GPU).  Each thread keeps a reference `base` (the largest
-// z c it has seen, or nearly), s = sum exp2(t) and w = sum t exp2(t) with
-// t = z c - base, c = log2(e) / T, one fused multiply-add, and the count of
-// values above z_t.  base is a value in fp32 to which the results are relative,
-// so it cancels; but it is z c rounded, and the largest term is 2 to the power
-// of what the rounding took away, up to half a unit of base's last place.  So
-// |base| stops at FAR = 2^28, up to which that is 8.  Below -FAR a thread's terms are
-// as good as none beside any row's that has a value above it (a finite mask),
-// and a row that holds nothing within +-FAR (masked as a whole, or of a very
-// low temperature, or with an infinity) has its sums taken again from
-// differences z - max.  base moves only when a value exceeds it by more than
-// LAG, so that rescaling is rare.  Values below -1e30 / c count as that value.
+// rows still fill the GPU).  Each warp keeps the largest z it has seen and a
+// reference `base`, that z times c = log2(e) / T in fp32; each thread
+// s = sum exp2(t) and w = sum t exp2(t) with t = z c - base, one fused
+// multiply-add, and the count of values above z_t.  base moves with every
+// record of the warp, so that no term is above 1 (a reference that lags d
+// behind leaves errors of d 2^-24 in t and in w, which then cancel against
+// log s: rows with one token far above the others had log-probabilities above
+// 0 and entropies below it).  A warp's record is rarer than its threads', and
+// the branch is the whole warp's, so this costs less than a lagging reference
+// for each thread (513 rows of 151643 bf16 50.6 us, with it 51.9).
+//
+// The results are relative to base, so its rounding cancels; but the largest
+// term is 2 to the power of what the rounding took away, up to half a unit of
+// base's last place.  So |base| stops at FAR = 2^28, up to which that is 8.  Below
+// -FAR a warp's terms are as good as none beside any row's that has a value
+// above it (a finite mask), and a row that holds nothing within +-FAR (masked
+// as a whole, or of a very low temperature, or with an infinity) has its sums
+// taken again from differences z - max.  Values below -1e30 / c count as that
+// value.
 //
 // c is rounded to fp32, i.e. the sums are those of a temperature off by a
 // relative 2^-24; the log of the sum is corrected for that to first order with
@@ -55,7 +62,6 @@ constexpr int MAX_K = 32;
 constexpr int MAX_V = 1 << 24;
 constexpr int MAX_Q = 8;            // CTAs that share a row: a cluster
 constexpr int LIST = 512;           // entries ranked at the end: as many as 16 warps' lists hold
-constexpr float LAG = 64.f;
 constexpr float FAR = 268435456.f;  // 2^28: |base| stops here, the row is far
 constexpr float LOW = -1e30f;       // terms below this z c are none
 constexpr uint32_t LOWEST_KEY = 0x00800000u;   // of the lowest finite value
@@ -272,26 +278,30 @@ struct Round<__nv_bfloat16, N> {
   }
 };
 
-// Sums relative to a base (-inf: no values): s = sum 2^t, w = sum t 2^t,
-// t = z c - base.
+// The reference that goes with a largest value (one rounding, the same
+// wherever it is taken).
+__device__ __forceinline__ float base_of(float top, float c) { return fminf(fmaxf(__fmul_rn(top, c), -FAR), FAR); }
+
+// Sums of values up to `top` (-inf: none): s = sum 2^t, w = sum t 2^t,
+// t = z c - base_of(top, c).
 struct Sums {
-  float base;
+  float top;
   int cnt;
   double s, w;
 
-  // Over groups of G lanes, relative to their largest base.
+  // Over groups of G lanes, relative to their largest value's base.
   template <int G>
-  __device__ __forceinline__ void reduce() {
-    float big = base;
+  __device__ __forceinline__ void reduce(float c) {
+    float big = top;
 #pragma unroll
     for (int off = G / 2; off; off >>= 1) big = fmaxf(big, __shfl_xor_sync(FULL, big, off));
-    if (base != -INFINITY && base != big) {
-      const float d = base - big;
+    if (top != -INFINITY && top != big) {
+      const float d = base_of(top, c) - base_of(big, c);
       const double f = ex2(d);
       w = f > 0.0 ? f * (w + d * s) : s * 0.0;
       s *= f;
     }
-    base = big;
+    top = big;
 #pragma unroll
     for (int off = G / 2; off; off >>= 1) {
       s += __shfl_xor_sync(FULL, s, off);
@@ -320,6 +330,9 @@ __device__ __forceinline__ double log_sum(double x) {
   }
   return e * LN2 + static_cast<double>(log1pf(static_cast<float>(mant - 1.0)));
 }
+
+// A log-probability without the sign that rounding could give it; a NaN stays.
+__device__ __forceinline__ float not_above_0(double x) { return x > 0.0 ? 0.f : static_cast<float>(x); }
 
 // The token asked for in a row: what it is read from, then what it is and
 // whether the row is asked for at all.
@@ -379,32 +392,16 @@ __device__ __forceinline__ void rank_entries(const uint64_t* list, int n, int K,
   }
 }
 
-// The sums of a row from differences to its maximum, by one CTA: for rows
-// whose largest value times c is beyond FAR.  Returns the maximum; s and w in
-// every thread.
+// The sums of a row from differences to its maximum m, by one CTA: for rows
+// where m c is beyond FAR.  s and w in every thread.
 template <typename Z, int NT, typename SharedT>
-__device__ __noinline__ float far_sums(const Z* z, int V, float c, SharedT& sh, double& s, double& w) {
+__device__ __noinline__ void far_sums(const Z* z, int V, float c, float m, SharedT& sh, double& s, double& w) {
   constexpr int E = Vec<Z>::E;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(Z)), n_vec = (V + lead + E - 1) / E;
-  float m = -INFINITY;
-#pragma unroll 4
-  for (int v = threadIdx.x; v < n_vec; v += NT) {
-    float y[E];
-    Vec<Z>::unpack(load_vec(z, v * E - lead, V), y);
-#pragma unroll
-    for (int j = 0; j < E; ++j) m = fmaxf(m, y[j]);
-  }
-  m = warp_max(m);
-  __syncthreads();
-  if (lane == 0) sh.part[warp].base = m;
-  __syncthreads();
-  for (int k = 0; k < NT / 32; ++k) m = fmaxf(m, sh.part[k].base);
   s = w = 0.0;
-#pragma unroll 4
-  for (int v = threadIdx.x; v < n_vec; v += NT) {
+  auto add = [&](const uint4& u) {
     float y[E], se = 0.f, we = 0.f;
-    Vec<Z>::unpack(load_vec(z, v * E - lead, V), y);
+    Vec<Z>::unpack(u, y);
 #pragma unroll
     for (int j = 0; j < E; ++j) {   // outside the row -inf: a term of 0
       const float t = max_nan((y[j] - m) * c, -200.f);
@@ -414,7 +411,14 @@ __device__ __noinline__ float far_sums(const Z* z, int V, float c, SharedT& sh, 
     }
     s += se;   // a vector's terms in fp32, vectors in fp64
     w += we;
-  }
+  };
+  const int lead = static_cast<int>((reinterpret_cast<uintptr_t>(z) & 15) / sizeof(Z));
+  const int begin = lead > 0 ? 1 : 0, end = (V + lead) / E;   // vectors inside the row whole
+  const uint4* zv = reinterpret_cast<const uint4*>(z - lead);
+#pragma unroll 4
+  for (int v = begin + static_cast<int>(threadIdx.x); v < end; v += NT) add(__ldg(zv + v));
+  if (threadIdx.x == 0 && lead > 0) add(load_vec(z, -lead, V));
+  if (threadIdx.x == 0 && end >= begin && end * E - lead < V) add(load_vec(z, end * E - lead, V));
   for (int off = 16; off; off >>= 1) {
     s += __shfl_xor_sync(FULL, s, off);
     w += __shfl_xor_sync(FULL, w, off);
@@ -429,7 +433,6 @@ __device__ __noinline__ float far_sums(const Z* z, int V, float c, SharedT& sh, 
     s += sh.part[k].s;
     w += sh.part[k].w;
   }
-  return m;
 }
 
 // NT threads with U vectors each a round, S rounds in the ring.
@@ -531,7 +534,8 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
 
   const F2 c2(p.c, p.c);
   F2 s2[2] = {F2(0.f, 0.f), F2(0.f, 0.f)}, w2[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
-  float base = 0.f, seen = -INFINITY, tau = -INFINITY;
+  float base = 0.f, top = -INFINITY;   // the warp's
+  float seen = -INFINITY, tau = -INFINITY;
   uint32_t tau_key = 0;
   int cnt = 0, bounds = 0, notes = 0, next_bound = 0;
   // s and w relative to another base, d below
@@ -572,11 +576,10 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
     take(r);
     fetch(r + S - 1);
     const float m = x.largest();
-    if (m > seen) {
-      const float to = fminf(fmaxf(m * p.c, -FAR), FAR);
-      if (seen == -INFINITY) {
-        base = to;
-      } else if (to - base > LAG) {
+    seen = fmaxf(seen, m);   // a NaN is not seen
+    if (__any_sync(FULL, m > top)) {
+      const float now = warp_max(seen), to = base_of(now, p.c);
+      if (top != -INFINITY) {   // else all sums are 0
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float s0, s1, w0, w1;
@@ -587,9 +590,9 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
           s2[k] = F2(s0, s1);
           w2[k] = F2(w0, w1);
         }
-        base = to;
       }
-      seen = m;
+      base = to;
+      top = now;
     }
     const bool bounding = p.K > 0 && r == next_bound;
     if (bounding) publish();
@@ -682,9 +685,6 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
     add2(w2[0], w2[1]).get(w, w1);
     s += s1;
     w += w1;
-    const float own = seen == -INFINITY ? -INFINITY : base;
-    const float big = warp_max(own);
-    if (own != -INFINITY && own != big) rescale(own - big, s, w);
     // five levels in fp32, 2^-24 each; across warps and CTAs fp64
 #pragma unroll
     for (int off = 16; off; off >>= 1) {
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
       w += __shfl_xor_sync(FULL, w, off);
     }
     cnt = __reduce_add_sync(FULL, cnt);
-    if (lane == 0) sh.part[warp] = Sums{big, cnt, s, w};
+    if (lane == 0) sh.part[warp] = Sums{top, cnt, s, w};
   }
   __syncthreads();
   if (p.K > 0) {
@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
   Sums sum;
   if (warp == 0) {
     sum = sh.part[lane & (NW - 1)];
-    sum.template reduce<NW>();
+    sum.template reduce<NW>(p.c);
   }
   if (Q > 1) {
     // hand list and sums to the cluster's first CTA
@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
     if (warp == 0) {
       const int i = lane & (MAX_Q - 1);
       sum = i < Q ? sh.sums[i] : Sums{-INFINITY, 0, 0.0, 0.0};
-      sum.template reduce<MAX_Q>();
+      sum.template reduce<MAX_Q>(p.c);
     } else if (p.K > 0) {
       // the largest of the CTAs' K-th entries bounds the row's K-th from below
       uint64_t least = lane < Q ? sh.all[lane * MAX_K + p.K - 1] : 0;
@@ -773,9 +773,9 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
     rank_entries<NT>(sh.list, n, p.K, [&](int rank, uint64_t e) { sh.all[rank] = e; });
 
   // the row's results but for the alternatives, by one lane
-  auto finish = [&](double origin) {
-    const bool dead = sum.base == -INFINITY && sum.s == 0.0;
-    const double from = dead ? 0.0 : sum.base;
+  auto finish = [&](double origin, float base_all) {
+    const bool dead = sum.top == -INFINITY && sum.s == 0.0;
+    const double from = dead ? 0.0 : base_all;
     const double mean_t = sum.w * recip(sum.s);
     const double log_s0 = log_sum(sum.s);
     const double log_s = dead ? 0.0 : log_s0 + (p.per_t - LN2) * mean_t;
@@ -783,29 +783,35 @@ __global__ void __launch_bounds__(NT, CTAS) logprobs_kernel(const Args p) {
     sh.base = from;
     sh.log_s = log_s;
     if (p.lse != nullptr) p.lse[row] = static_cast<float>(dead ? -INFINITY : origin * p.inv_t + from * p.per_t + log_s);
-    if (p.entropy != nullptr) p.entropy[row] = static_cast<float>(dead ? 0.0 : log_s0 - mean_t * LN2);
+    if (p.entropy != nullptr) p.entropy[row] = dead ? 0.f : 0.f - not_above_0(mean_t * LN2 - log_s0);
     if (p.logp != nullptr) {
       const double v = ((zt - origin) * p.c - from) * p.per_t - log_s;
-      p.logp[row] = bad_token ? __int_as_float(0x7fc00000) : static_cast<float>(v);
+      p.logp[row] = bad_token ? __int_as_float(0x7fc00000) : not_above_0(v);
     }
     if (p.rank != nullptr) p.rank[row] = bad_token ? 0 : sum.cnt + 1;
   };
-  const bool far = tid == 0 && !(fabsf(sum.base) < FAR) && sum.base != -INFINITY;
-  if (tid == 0 && !far) finish(0.0);
+  const float base_all = sum.top == -INFINITY ? -INFINITY : base_of(sum.top, p.c);
+  const bool far = tid == 0 && !(fabsf(base_all) < FAR) && sum.top != -INFINITY;
+  if (tid == 0) {
+    if (far)
+      sh.origin = sum.top;
+    else
+      finish(0.0, base_all);
+  }
   if (__syncthreads_or(far)) {
+    const double origin = sh.origin;
     double s, w;
-    const double origin = far_sums<Z, NT>(z, p.V, p.c, sh, s, w);
-    sum.base = 0.f;
+    far_sums<Z, NT>(z, p.V, p.c, static_cast<float>(origin), sh, s, w);
     sum.s = s;
     sum.w = w;
-    if (tid == 0) finish(origin);
+    if (tid == 0) finish(origin, 0.f);
     __syncthreads();
   }
   if (p.K == 0) return;
   if (Q > 1) n = sh.n_all;   // the first warp's too
   auto out = [&](int rank, uint64_t e) {
     const size_t o = static_cast<size_t>(row) * p.K + rank;
-    p.top_logp[o] = static_cast<float>(((value_of(e) - sh.origin) * p.c - sh.base) * p.per_t - sh.log_s);
+    p.top_logp[o] = not_above_0(((value_of(e) - sh.origin) * p.c - sh.base) * p.per_t - sh.log_s);
     p.top_idx[o] = index_of(e);
   };
   if (tid < min(n, p.K)) out(tid, sh.all[tid]);

@@ -474,7 +474,8 @@ int dflash_gemm_i8(const int8_t* A, const float* sa, const int8_t* B, const floa
  * logp, entropy, lse [M] fp32, rank [M] int32, top_logp [M, K] fp32, top_idx
  * [M, K] int32; every output is nullable (top_logp and top_idx: both or
  * neither; neither when K == 0).  1 <= M, 1 <= V <= 16777216,
- * 0 <= K <= min(32, V), 1e-6 <= T = temperature <= 1e6.  Sums are fp32 within
+ * 0 <= K <= min(32, V), 1e-6 <= T = temperature <= 1e6.  Log-probabilities
+ * are never above 0 and entropies never below it.  Sums are fp32 within
  * a warp and fp64 across warps; results are the same bit for bit from run to
  * run.
  */

@@ -18,7 +18,7 @@ pytestmark = pytest.mark.gpu
 
 MASKS = [-1e4, -1e5, -1e9, -1e10, -1e12, -1e20, -1e28, -1e30, -3e38]
 # (V, copies of the 14 rows), fp32 and bf16 fall into the same form but for the length of a vector
-FORMS = [(40, 1), (1000, 1), (5000, 1), (140000, 1), (9000, 12), (20000, 20), (40000, 20), (5000, 25), (20000, 70), (900, 25),
+FORMS = [(3, 1), (40, 1), (1000, 1), (5003, 1), (140000, 1), (9000, 12), (20000, 20), (40000, 20), (5000, 25), (20000, 70), (900, 25),
          (3000, 90)]
 
 
