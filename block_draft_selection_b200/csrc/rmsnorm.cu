@@ -25,6 +25,11 @@
 // halves stay halves or err upwards: those are x = a/2 (q = 63.5, even
 // neighbour 64) and, where a is 127 times a power of two, exact products.
 // 127 / a is therefore rounded up.
+//
+// Where the sum of squares overflows fp32, r is taken in fp64, and h, whose
+// product with gamma may overflow too, goes on as h 2^-66, exact but for values
+// that are nothing beside the row's, with r 2^66.  Elsewhere |h| < 2^64, so that
+// |h gamma| is finite for every |gamma| < 2^64.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -53,6 +58,18 @@ struct Args {
 };
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// |h gamma| of a vector's values joined to the maximum a; NaN if one is.
+__device__ __forceinline__ float join_max(float a, const uint4& h, const uint4& g) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float u, v;
+    mul2(widen2(word(h, i)), widen2(word(g, i))).get(u, v);
+    a = max_nan(a, fabsf(u));
+    a = max_nan(a, fabsf(v));
+  }
+  return a;
+}
 
 __device__ __forceinline__ uint32_t narrow2(F2 f) {
   float a, b;
@@ -130,14 +147,9 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_kernel(const Args p) {
       const uint32_t w = word(hv[j], i);
       const F2 f = widen2(w);
       if (NORM) s2 = fma2(f, f, s2);
-      if (I8 && NORM) {
-        float u, v;
-        mul2(f, widen2(word(g, i))).get(u, v);
-        a = max_nan(a, fabsf(u));
-        a = max_nan(a, fabsf(v));
-      }
       if (I8 && !NORM) m2 = __hmax2_nan(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
     }
+    if (I8 && NORM) a = join_max(a, hv[j], g);
     if (I8 && !NORM) a = max_nan(a, max_nan(__low2float(m2), __high2float(m2)));
   }
   float ss, s1;
@@ -168,7 +180,7 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_kernel(const Args p) {
     if (ss < INFINITY) {
       r = rsqrtf(fmaf(ss, p.inv_d, p.eps));   // off by 2 units in the last place at most
     } else {
-      // fp32 overflowed (or the row holds a NaN or an infinity): again in fp64
+      // fp32 overflowed (or the row holds a NaN or an infinity), the same in every thread: again in fp64
       double s = 0.0;
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
@@ -183,11 +195,33 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_kernel(const Args p) {
       for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(FULL, s, off);
       if (nwarps > 1) {
         if (lane == 0) red_d[warp] = s;
-        __syncthreads();   // uniform: every thread holds the same ss
+        __syncthreads();
         s = 0.0;
         for (int w = 0; w < nwarps; ++w) s += red_d[w];
       }
-      r = static_cast<float>(1.0 / sqrt(s / (8 * p.d8) + static_cast<double>(p.eps)));
+      const double r64 = 1.0 / sqrt(s / (8 * p.d8) + static_cast<double>(p.eps));
+      r = static_cast<float>(r64);
+      if (!I8 || a == INFINITY) {   // a, the same in every thread, again too
+        r = static_cast<float>(r64 * 0x1p66);
+        a = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+          const int c = tid + j * blockDim.x;
+          const F2 k(0x1p-66f, 0x1p-66f);
+          hv[j] = make_uint4(narrow2(mul2(widen2(hv[j].x), k)), narrow2(mul2(widen2(hv[j].y), k)),
+                             narrow2(mul2(widen2(hv[j].z), k)), narrow2(mul2(widen2(hv[j].w), k)));
+          if (I8 && c < p.d8) a = join_max(a, hv[j], __ldg(p.gamma + c));
+        }
+        if (I8) {
+#pragma unroll
+          for (int off = 16; off; off >>= 1) a = max_nan(a, __shfl_xor_sync(FULL, a, off));
+          if (nwarps > 1) {
+            if (lane == 0) red_a[warp] = a;   // the first ones were read before the last barrier
+            __syncthreads();
+            for (int w = 0; w < nwarps; ++w) a = max_nan(a, red_a[w]);
+          }
+        }
+      }
     }
   }
   if (I8) {

@@ -396,7 +396,9 @@ int dflash_verify(const int32_t* draft, const int32_t* target, int B, int L, int
  * x, residual, h, y [M, d] bf16; gamma [d] bf16; residual NULL: none, and h
  * must be NULL then; h NULL: the sum is not written.  h and y may each be the
  * same array as x or as residual (not each other); any other overlap is not
- * allowed.  A sum of squares beyond fp32's range is taken in fp64.
+ * allowed.  A sum of squares beyond fp32's range is taken in fp64, and the
+ * products h * gamma stay in range for every |gamma| < 2^64; products below
+ * 2^-126 are rounded as fp32 rounds them.
  * Requires M >= 1, 8 <= d <= 32768, d % 8 == 0, eps finite and >= 1e-20,
  * 16-byte aligned pointers.
  */
@@ -411,8 +413,8 @@ int dflash_rmsnorm(const dflash_bf16* x, const dflash_bf16* residual, const dfla
  * (r cancels in q; halves round to even, decided exactly), so that
  * q * scale is the normalised row to within half a step.  q is in
  * [-127, 127].  A row with a < 2^-100 gives q = 0 and scale = 0; a row that
- * holds a NaN or an infinity (after the product with gamma) gives q = 0 and
- * scale = NaN, which a product taken from it carries on.
+ * holds a NaN or an infinity (or where gamma makes one, from |gamma| of 2^64
+ * on) gives q = 0 and scale = NaN, which a product taken from it carries on.
  * q [M, d] int8 (8-byte aligned), scale [M] fp32; the rest as dflash_rmsnorm.
  */
 int dflash_rmsnorm_i8(const dflash_bf16* x, const dflash_bf16* residual, const dflash_bf16* gamma, float eps, int M,
