@@ -33,6 +33,7 @@ import argparse
 import hashlib
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -105,10 +106,28 @@ def lmhead_algorithmic(w: syn.Workload):
     return bytes_, flops
 
 
+CSRC = os.path.join(ROOT, "block_draft_selection_b200", "csrc")
+
+
+def kernel_sources(name="lmhead_topk.cu"):
+    """The kernel's source file and every file of its folder that it includes, directly or not.  (include/dflash.h,
+    which holds prototypes and status codes, is not one of them.)"""
+    found, todo = [], [name]
+    while todo:
+        f = todo.pop(0)
+        if f in found:
+            continue
+        found.append(f)
+        with open(os.path.join(CSRC, f)) as fh:
+            included = re.findall(r'^\s*#\s*include\s+"([^"]+)"', fh.read(), re.M)
+        todo += [i for i in included if os.path.dirname(i) == ""]
+    return found
+
+
 def kernel_source_hash():
     h = hashlib.sha256()
-    for name in ("lmhead_topk.cu", "common.cuh"):
-        with open(os.path.join(ROOT, "block_draft_selection_b200", "csrc", name), "rb") as f:
+    for name in kernel_sources():
+        with open(os.path.join(CSRC, name), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
 
