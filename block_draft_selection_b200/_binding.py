@@ -686,7 +686,8 @@ def dflash_token_logprobs(logits, tokens=None, K=K_TOP, temperature=1.0, logp=No
     """Log-probabilities of one given token per row of logits [M,V] (f32 or bf16; rows may be strided), with the
     token's rank, the row's entropy and log-sum-exp, and its K best tokens.  tokens [M] i32 (negative: the row is
     not asked for, its outputs stay as they are) or None.  Returns (logp [M], rank [M] i32, entropy [M], lse [M],
-    top_logp [M,K], top_idx [M,K] i32); logp and rank are None without tokens."""
+    top_logp [M,K], top_idx [M,K] i32); logp and rank are None without tokens.  With tokens and no output given, all of
+    them are parts of one buffer: keeping or saving one keeps or saves all (clone() it, or pass outputs)."""
     pz, z_bf16, ld, M, V, index = _logits(logits, "logits")
     pt = None if tokens is None else _arg(tokens, "tokens", torch.int32, (M,), index)
     outs, ptrs = _logprob_outs((M,), K, index, stream, logp, rank, entropy, lse, top_logp, top_idx, tokens is not None)
@@ -700,7 +701,8 @@ def dflash_emitted_logprobs(target_logits, draft, accept_len, next_token, K=K_TO
                             stream=None):
     """dflash_token_logprobs for the tokens that a verification step emitted: draft [B,L], accept_len [B],
     next_token [B] i32 and the target_logits [B*(L+1),V] they were verified against.  Outputs [B,L+1] (and
-    [B,L+1,K]); positions at and past accept_len stay as they are (zero where the call allocates)."""
+    [B,L+1,K]); positions at and past accept_len stay as they are (zero where the call allocates).  With no output
+    given, all of them are parts of one buffer, as dflash_token_logprobs says."""
     pz, z_bf16, ld, rows, V, index = _logits(target_logits, "target_logits")
     (B, L), _, pd = _matrix(draft, "draft", torch.int32)
     if rows != B * (L + 1):
