@@ -464,8 +464,8 @@ int dflash_gemm_i8(const int8_t* A, const float* sa, const int8_t* B, const floa
  * (log-probability -inf, no entropy); in a row with nothing but -inf, lse and
  * every log-probability are -inf, the entropy is 0.  Finite masks of any size
  * are values like others (a row of nothing but one is uniform).  A row whose
- * largest |z| is above about 1.8e8 T is read a second time.  A NaN or +inf in a
- * row makes its lse, entropy and log-probabilities NaN; a NaN counts as the
+ * largest value lies beyond +-1.8e8 T is read a second time.  A NaN or +inf in
+ * a row makes its lse, entropy and log-probabilities NaN; a NaN counts as the
  * largest value in top_idx.
  * tokens [M] int32: a negative one marks a row that is not asked for (padding
  * of a batch): its outputs keep what they held (its logits may be read, with
